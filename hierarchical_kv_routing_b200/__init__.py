@@ -26,7 +26,8 @@ __all__ = ["HGAParams", "KVCache", "load", "lib_path", "hga_build_summaries", "h
            "decode_workspace", "hga_forward_prefill_hostkv", "HGAError", "PREFILL",
            "DECODE", "PREFILL_HOSTKV", "ATTEND_BACKWARD", "hga_device_status",
            "hga_hostkv_link_bytes", "hga_attend_backward", "hga_hostkv_plan",
-           "hostkv_workspace_bytes"]
+           "hostkv_workspace_bytes", "HGARope", "PagedKVCache", "hga_paged_plan",
+           "hga_qk_norm_rope", "hga_qk_norm_rope_backward", "hga_paged_decode"]
 
 PREFILL, DECODE, PREFILL_HOSTKV, ATTEND_BACKWARD = 0, 1, 2, 3
 _F32, _BF16 = 0, 1
@@ -134,6 +135,7 @@ def load():
         for f in ("hga_build_summaries", "hga_route", "hga_attend", "hga_forward",
                   "hga_attend_backward"):
             getattr(lib, f).restype = ctypes.c_int
+        _declare_paged(lib)
         _lib = lib
         return lib
 
@@ -680,3 +682,7 @@ def hga_forward(mode: int, *args, **kw):
     if mode == PREFILL_HOSTKV:
         return hga_forward_prefill_hostkv(*args, **kw)
     raise HGAError(f"unknown mode {mode}")
+
+
+from .paged import (HGARope, PagedKVCache, declare as _declare_paged, hga_paged_decode,  # noqa: E402
+                    hga_paged_plan, hga_qk_norm_rope, hga_qk_norm_rope_backward)

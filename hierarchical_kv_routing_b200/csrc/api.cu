@@ -9,6 +9,7 @@
 #include <utility>
 
 #include "hga_internal.cuh"
+#include "paged_internal.cuh"
 #include "route_common.cuh"
 
 namespace hga {
@@ -362,11 +363,14 @@ int hga_last_cuda_error(void) { return g_last_cuda_error; }
 hga_status hga_device_status(void *stream, int clear) {
     const cudaStream_t st = (cudaStream_t)stream;
     hga_status first = HGA_OK;
-    const hga_status parts[5] = {summaries_error_take(st, clear != 0),
+    const hga_status parts[8] = {summaries_error_take(st, clear != 0),
                                  attend_tc_error_take(st, clear != 0),
                                  decode_error_take(st, clear != 0),
                                  tier_error_take(st, clear != 0),
-                                 backward_error_take(st, clear != 0)};
+                                 backward_error_take(st, clear != 0),
+                                 plan_error_take(st, clear != 0),
+                                 qk_error_take(st, clear != 0),
+                                 paged_error_take(st, clear != 0)};
     for (hga_status p : parts)
         if (p != HGA_OK && first == HGA_OK) first = p;
     return first;

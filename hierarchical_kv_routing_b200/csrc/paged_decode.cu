@@ -1,0 +1,767 @@
+// Attention of one new token per sequence over a paged key/value cache.
+//
+//   o = sum_j softmax_j(scale q.k_j) v_j   over the visible tokens j of a row:
+//   j < len, and with a window w only j >= len - w or j < sinks.
+//
+// Bound by HBM: a visible key costs 2 D e bytes of K and V per KV head and
+// 4 D G FLOP, G FLOP per byte for bf16.  So every K and V row is read once for
+// all G query heads of its KV head, the products run on warp-level tensor-core
+// tiles (a new token has at most 16 rows of queries per KV head, below the
+// 64- and 128-row tiles of tcgen05), and the design is about keeping loads in
+// flight and every SM equally loaded.
+//
+// The visible tokens of a row are numbered 0 .. n-1 without a gap: the first
+// min(sinks, lo) and then lo .. len-1, lo = max(0, len - window).  Tiles, splits
+// and masks work on those numbers, so a windowed row costs what it attends, and
+// only a row's last tile is ragged.
+//
+// Split: an item is a sequence and the KV heads (and query heads) one CTA takes
+// together; its visible keys are cut into units.  The units of all items form one
+// line, of which CTA i of n takes [U i / n, U (i + 1) / n): every CTA has the
+// same work to one unit whatever the lengths are, and no length is read on the
+// host.  A CTA's range covers whole items, whose rows it writes itself, and at
+// most one item it continues and one it leaves open: those rows go to the
+// workspace, and k_paged_join adds them up in CTA order.
+//
+// A CTA is four warps that run on their own: each streams tiles of 4 KB of K and
+// 4 KB of V through a ring of kStages in shared memory (cp.async, 16 bytes a
+// lane), three deep, so two CTAs per SM keep 128 KB in flight, above the ~50 KB
+// that 7 TB/s and a microsecond of latency ask for.  The page of each key comes from the block table one tile
+// ahead of its loads.  Where Hkv allows, the four warps take the same keys of
+// adjacent heads (whole runs of a page's token rows) and never meet; else they
+// take every fourth tile of one head and are merged in shared memory.
+#include <algorithm>
+
+#include "paged_internal.cuh"
+
+namespace hga {
+
+__device__ int g_paged_error = 0;
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32, kStages = 3;
+constexpr int kTileBytes = 4096;             // of K, and of V, per warp and stage
+constexpr int kMaxCtas = 2 * 148;            // two per SM
+constexpr int kUnitTiles = 4;                // tiles of a unit, over the warps of one head
+
+struct Split {
+    int items;         // per sequence: Hkv / hw * gsplit
+    int hw, kw;        // KV heads per CTA, warps per KV head (hw * kw = kWarps)
+    int gsplit, gch;   // chunks of a KV head's query heads, heads per chunk
+    int rows;          // hw * gch: rows of an item
+    int n;             // CTAs
+    int by_item;       // join entries indexed by item (else by the CTA that starts it)
+    float *part;       // [n][2][rows][D]: continued and opened item, unnormalised
+    float2 *ml;        // [n][2][rows]: running maximum (base 2) and sum
+    int4 *join;        // entry: (sequence, item, first CTA, last CTA); first -1: not split
+};
+
+__device__ __forceinline__ uint32_t su32(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+// 16 bytes to shared memory; zeros, and no read, where live is false
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The visible tokens of a row: s first ones, then lo .. ; n in all.
+struct Visible {
+    int s, lo, n;
+};
+__device__ __forceinline__ Visible visible(const PagedArgs &A, int b) {
+    int len = A.lens[b];
+    if (len < 0 || (long long)len > ((long long)A.max_pages << A.log2_page)) len = 0;
+    Visible v;
+    v.lo = A.window > 0 ? max(0, len - A.window) : 0;
+    v.s = min(A.sinks, v.lo);
+    v.n = v.s + len - v.lo;
+    return v;
+}
+__device__ __forceinline__ int units_of(int n, int uk) { return n / uk + (n % uk != 0); }
+
+// A CTA's walk over its units: the segment [k0, k1) of item (b, it) that is next.
+struct Walk {
+    int b, it, u, nu, cnt;
+    long long left;
+    Visible v;
+    __device__ __forceinline__ void take() { cnt = (int)min((long long)(nu - u), left); }
+    __device__ __forceinline__ int k0(int uk) const { return u * uk; }
+    __device__ __forceinline__ int k1(int uk) const {
+        return u + cnt >= nu ? v.n : (u + cnt) * uk;
+    }
+    __device__ __forceinline__ bool next(const PagedArgs &A, const Split &S, int uk) {
+        left -= cnt;
+        if (left <= 0) return false;
+        u = 0;
+        if (++it == S.items) {
+            it = 0;
+            do {
+                if (++b >= A.B) return false;
+                v = visible(A, b);
+                nu = units_of(v.n, uk);
+            } while (nu == 0);
+        }
+        take();
+        return true;
+    }
+};
+
+// ---- bf16: m16n8k16 tiles.  S = Q K^T with the queries as the 16-row A operand
+// (rows beyond the chunk's heads are zero) and K rows as its columns; the S
+// accumulator, exponentiated and rounded, is the A operand of O += P V, V read
+// transposed.  Rows of shared memory are XOR-swizzled in 16-byte chunks so the
+// eight rows of an ldmatrix fall in different banks.  kRows = 8 leaves the upper
+// half of the tile out of everything but the products.
+template <int D, int kRows> struct TileBf16 {
+    using T = __nv_bfloat16;
+    static constexpr int kKeys = kTileBytes / (D * 2), kSwz = 7, kMerge = 8;
+    static constexpr int R = kRows / 8;
+    uint32_t q[D / 16][4];
+    float o[D / 8][4];
+    float m[R], l[R];
+
+    __device__ __forceinline__ void begin(const PagedArgs &A, int b, int head0, int heads) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = (lane & 3) * 2;
+        const T *base = static_cast<const T *>(A.q) + ((int64_t)b * A.Hq + head0) * D + c;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[i][j] = 0;
+            const T *p = base + i * 16;
+            if (g < heads) {
+                q[i][0] = *reinterpret_cast<const uint32_t *>(p + g * D);
+                q[i][2] = *reinterpret_cast<const uint32_t *>(p + g * D + 8);
+            }
+            if (R == 2 && g + 8 < heads) {
+                q[i][1] = *reinterpret_cast<const uint32_t *>(p + (g + 8) * D);
+                q[i][3] = *reinterpret_cast<const uint32_t *>(p + (g + 8) * D + 8);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) m[r] = -INFINITY, l[r] = 0.f;
+    }
+
+    // valid: bit k set if key k of the tile counts
+    __device__ __forceinline__ void tile(uint32_t ks, uint32_t vs, uint32_t valid, float scale,
+                                         float *) {
+        constexpr int NT = kKeys / 8;
+        const int lane = threadIdx.x & 31, c = (lane & 3) * 2;
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
+        // matrices of an x4 load: keys 0-7 and 8-15 of the pair, two chunks of 8 dimensions
+        const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t f[4];
+                ldsm4(f, ks + (n * 8 + krow) * (D * 2) + (((i * 2 + kch) ^ (lane & 7)) << 4));
+                mma16816(s[n], q[i], f[0], f[1]);
+                mma16816(s[n + 1], q[i], f[2], f[3]);
+            }
+        float top[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) top[r] = -INFINITY;
+        constexpr uint32_t full = kKeys == 32 ? 0xffffffffu : (1u << kKeys) - 1u;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2 * R; ++j) {
+                s[n][j] *= scale;
+                if (valid != full && !((valid >> (n * 8 + c + (j & 1))) & 1u)) s[n][j] = -INFINITY;
+                top[j >> 1] = fmaxf(top[j >> 1], s[n][j]);
+            }
+        bool grow = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+            // the reference moves only when the maximum passes it by 2^8: weights and
+            // sums stay far from fp32's range, and O is rarely rescaled
+            grow |= top[r] > m[r] + 8.f;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float nm = top[r] > m[r] + 8.f ? top[r] : m[r];
+                const float f = nm == -INFINITY ? 1.f : ex2(m[r] - nm);
+                m[r] = nm;
+                l[r] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    o[i][2 * r] *= f;
+                    o[i][2 * r + 1] *= f;
+                }
+            }
+        }
+        float ref[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) ref[r] = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2 * R; ++j) {
+                s[n][j] = ex2(s[n][j] - ref[j >> 1]);
+                l[j >> 1] += s[n][j];
+            }
+        const int vrow = lane & 15, vch = lane >> 4;
+#pragma unroll
+        for (int kb = 0; kb < kKeys / 16; ++kb) {
+            // the weights are rounded to bf16 (at most half a step, 2^-8 relative) for the product;
+            // their sum above is of the unrounded ones
+            uint32_t p[4] = {pack2(s[2 * kb][0], s[2 * kb][1]), 0u,
+                             pack2(s[2 * kb + 1][0], s[2 * kb + 1][1]), 0u};
+            if (R == 2) {
+                p[1] = pack2(s[2 * kb][2], s[2 * kb][3]);
+                p[3] = pack2(s[2 * kb + 1][2], s[2 * kb + 1][3]);
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t f[4];
+                ldsm4_t(f, vs + (kb * 16 + vrow) * (D * 2) + (((i * 2 + vch) ^ (lane & 7)) << 4));
+                mma16816(o[2 * i], p, f[0], f[1]);
+                mma16816(o[2 * i + 1], p, f[2], f[3]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void end() {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        }
+    }
+    // rows round * kMerge .. + kMerge of this warp
+    __device__ __forceinline__ void put(int round, float *rows, float2 *ml) const {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = (lane & 3) * 2;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (r == round) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    *reinterpret_cast<float2 *>(rows + g * D + i * 8 + c) =
+                        make_float2(o[i][2 * r], o[i][2 * r + 1]);
+                if ((lane & 3) == 0) ml[g] = make_float2(m[r], l[r]);
+            }
+    }
+};
+
+// ---- fp32: CUDA cores.  A group of eight lanes takes a key (four keys at a
+// time), each lane 16 bytes of every 128; scores are summed over the group, the
+// weights pass through shared memory, and for P V a lane owns four dimensions
+// (with D = 64 the half-warps take alternate halves of the tile's keys).
+template <int D, int kRows> struct TileF32 {
+    using T = float;
+    static constexpr int kKeys = kTileBytes / (D * 4), kSwz = 0, kMerge = 4;
+    static constexpr int QC = D / 32, KG = kKeys / 4, LPR = D / 4;   // lanes per V row
+    static constexpr int VK = kKeys * LPR / 32;                        // V rows per lane
+    float4 q[kRows][QC];
+    float4 o[kRows];
+    float m[kRows], l[kRows];
+
+    __device__ __forceinline__ void begin(const PagedArgs &A, int b, int head0, int heads) {
+        const int lane = threadIdx.x & 31;
+        const float *base = static_cast<const float *>(A.q) + ((int64_t)b * A.Hq + head0) * D;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+#pragma unroll
+            for (int i = 0; i < QC; ++i)
+                q[r][i] = r < heads ? *reinterpret_cast<const float4 *>(base + r * D + i * 32 +
+                                                                         (lane & 7) * 4)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void tile(uint32_t ks_, uint32_t vs_, uint32_t valid, float scale,
+                                         float *ps) {
+        const int lane = threadIdx.x & 31, l8 = lane & 7, kg = lane >> 3;
+        const float *ks = static_cast<const float *>(__cvta_shared_to_generic(ks_));
+        const float *vs = static_cast<const float *>(__cvta_shared_to_generic(vs_));
+        float s[KG][kRows];
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+            float4 x[QC];
+#pragma unroll
+            for (int i = 0; i < QC; ++i)
+                x[i] = *reinterpret_cast<const float4 *>(ks + (k * 4 + kg) * D + i * 32 + l8 * 4);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                float a = 0.f;
+#pragma unroll
+                for (int i = 0; i < QC; ++i) {
+                    a = fmaf(q[r][i].x, x[i].x, a);
+                    a = fmaf(q[r][i].y, x[i].y, a);
+                    a = fmaf(q[r][i].z, x[i].z, a);
+                    a = fmaf(q[r][i].w, x[i].w, a);
+                }
+                s[k][r] = a;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+            const bool live = (valid >> (k * 4 + kg)) & 1u;
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                s[k][r] += __shfl_xor_sync(0xffffffffu, s[k][r], 1);
+                s[k][r] += __shfl_xor_sync(0xffffffffu, s[k][r], 2);
+                s[k][r] += __shfl_xor_sync(0xffffffffu, s[k][r], 4);
+                s[k][r] = live ? s[k][r] * scale : -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            float top = s[0][r];
+#pragma unroll
+            for (int k = 1; k < KG; ++k) top = fmaxf(top, s[k][r]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            if (top > m[r] + 8.f) {            // the same in every lane
+                const float f = ex2(m[r] - top);
+                m[r] = top;
+                l[r] *= f;
+                o[r].x *= f, o[r].y *= f, o[r].z *= f, o[r].w *= f;
+            }
+            const float ref = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+            for (int k = 0; k < KG; ++k) {
+                const float p = ex2(s[k][r] - ref);
+                l[r] += p;
+                if (l8 == r) ps[r * kKeys + k * 4 + kg] = p;
+            }
+        }
+        __syncwarp();
+        const int k0 = LPR == 32 ? 0 : (lane / LPR) * VK;
+        float4 x[VK];
+#pragma unroll
+        for (int k = 0; k < VK; ++k)
+            x[k] = *reinterpret_cast<const float4 *>(vs + (k0 + k) * D + (lane % LPR) * 4);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int k4 = 0; k4 < VK; k4 += 4) {
+                const float4 p = *reinterpret_cast<const float4 *>(ps + r * kKeys + k0 + k4);
+                const float pk[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    o[r].x = fmaf(pk[j], x[k4 + j].x, o[r].x);
+                    o[r].y = fmaf(pk[j], x[k4 + j].y, o[r].y);
+                    o[r].z = fmaf(pk[j], x[k4 + j].z, o[r].z);
+                    o[r].w = fmaf(pk[j], x[k4 + j].w, o[r].w);
+                }
+            }
+        __syncwarp();
+    }
+
+    __device__ __forceinline__ void end() {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
+            if (LPR == 16) {
+                o[r].x += __shfl_xor_sync(0xffffffffu, o[r].x, 16);
+                o[r].y += __shfl_xor_sync(0xffffffffu, o[r].y, 16);
+                o[r].z += __shfl_xor_sync(0xffffffffu, o[r].z, 16);
+                o[r].w += __shfl_xor_sync(0xffffffffu, o[r].w, 16);
+            }
+        }
+    }
+    __device__ __forceinline__ void put(int round, float *rows, float2 *ml) const {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+            if (r / kMerge == round) {
+                if (lane < LPR)
+                    *reinterpret_cast<float4 *>(rows + (r % kMerge) * D + lane * 4) = o[r];
+                if (lane == 0) ml[r % kMerge] = make_float2(m[r], l[r]);
+            }
+    }
+};
+
+template <typename Tile, int D> constexpr size_t smem_bytes() {
+    return (size_t)kWarps * kStages * 2 * kTileBytes + (size_t)kWarps * Tile::kMerge * D * 4;
+}
+
+template <typename T> __device__ __forceinline__ void put4(T *p, float4 x);
+template <> __device__ __forceinline__ void put4<float>(float *p, float4 x) {
+    *reinterpret_cast<float4 *>(p) = x;
+}
+template <> __device__ __forceinline__ void put4<__nv_bfloat16>(__nv_bfloat16 *p, float4 x) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
+}
+
+constexpr float kLn2 = 0.693147180559945f;
+
+template <typename Tile, int D, int kRows>
+__global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A, const Split S) {
+    using T = typename Tile::T;
+    constexpr int kKeys = Tile::kKeys, kCpr = D * (int)sizeof(T) / 16, kLoads = kTileBytes / 512;
+    extern __shared__ __align__(1024) char ring[];
+    __shared__ int start[4];                       // b, item, unit of the CTA's first unit
+    __shared__ uint32_t valid[kWarps][kStages];
+    __shared__ float2 ml[kWarps][Tile::kMerge];
+    __shared__ __align__(16) float ps[sizeof(T) == 4 ? kWarps * kRows * kKeys : 1];
+    float *merge = reinterpret_cast<float *>(ring + kWarps * kStages * 2 * kTileBytes);
+    long long *sums = reinterpret_cast<long long *>(ring);   // before the ring is in use
+
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    const int uk = kUnitTiles * kKeys;
+    // ---- where this CTA's units begin: sums over runs of sequences, one per thread
+    const int per = (A.B + kThreads - 1) / kThreads;
+    const int r0 = min(A.B, tid * per), r1 = min(A.B, r0 + per);
+    long long mine = 0;
+    for (int b = r0; b < r1; ++b) mine += (long long)units_of(visible(A, b).n, uk) * S.items;
+    sums[tid] = mine;
+    if (tid < 4) start[tid] = -1;
+    __syncthreads();
+    long long before = 0, U = 0;
+    for (int t = 0; t < kThreads; ++t) {
+        if (t < tid) before += sums[t];
+        U += sums[t];
+    }
+    // with fewer units than CTAs the last ones take none, so that a split item's
+    // parts lie in CTAs without a gap
+    const long long n = U < S.n ? U : S.n;
+    const long long u0 = cta < n ? U * cta / n : 0, u1 = cta < n ? U * (cta + 1) / n : 0;
+    if (u0 < u1 && u0 >= before && u0 < before + mine) {
+        long long at = u0 - before;
+        for (int b = r0; b < r1; ++b) {
+            const int nu = units_of(visible(A, b).n, uk);
+            if (at < (long long)nu * S.items) {
+                start[0] = b;
+                start[1] = (int)(at / nu);
+                start[2] = (int)(at % nu);
+                break;
+            }
+            at -= (long long)nu * S.items;
+        }
+    }
+    // rows of empty sequences, shared out over the CTAs; bad lengths are reported here
+    for (int b = cta; b < A.B; b += gridDim.x) {
+        const Visible v = visible(A, b);
+        if (v.n) continue;
+        if (tid == 0 && A.lens[b] != 0) atomicExch(&g_paged_error, (int)HGA_ERR_BOUNDS);
+        T *o = static_cast<T *>(A.out) + (int64_t)b * A.Hq * D;
+        for (int i = tid; i < A.Hq * D / 4; i += kThreads)
+            put4<T>(o + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int h = tid; A.lse && h < A.Hq; h += kThreads)
+            A.lse[(int64_t)b * A.Hq + h] = -INFINITY;
+        if (S.by_item)
+            for (int i = tid; i < S.items; i += kThreads)
+                S.join[(int64_t)b * S.items + i] = make_int4(0, 0, -1, -1);
+    }
+    __syncthreads();
+    if (u0 >= u1) {
+        if (tid == 0 && !S.by_item) S.join[cta] = make_int4(0, 0, -1, -1);
+        return;
+    }
+
+    Walk C;
+    C.b = start[0], C.it = start[1], C.u = start[2];
+    C.left = u1 - u0;
+    C.v = visible(A, C.b);
+    C.nu = units_of(C.v.n, uk);
+    C.take();
+    Walk P = C;
+    const int hsub = warp % S.hw, ksub = warp / S.hw;
+    char *kring = ring + warp * kStages * 2 * kTileBytes;
+    const uint32_t ring_s = su32(kring);
+    const int64_t row_bytes = (int64_t)A.Hkv * D * (int)sizeof(T);
+    const int page_mask = (1 << A.log2_page) - 1;
+
+    // ---- producer: the next tile's page entries are read one tile ahead of its rows
+    int pk = P.k0(uk) + ksub * kKeys, pk1 = P.k1(uk);
+    bool plive = true;                              // false: no tile left
+    int ptok = 0, ppage = 0, phead = 0;
+    bool pin = false;
+    auto fetch = [&]() {
+        while (pk >= pk1) {
+            if (!P.next(A, S, uk)) {
+                plive = false;
+                return;
+            }
+            pk = P.k0(uk) + ksub * kKeys;
+            pk1 = P.k1(uk);
+        }
+        const int key = pk + (lane & (kKeys - 1));
+        pin = key < pk1;
+        ptok = key < P.v.s ? key : key - P.v.s + P.v.lo;
+        ppage = pin ? A.table[(int64_t)P.b * A.max_pages + (ptok >> A.log2_page)] : 0;
+        phead = (P.it / S.gsplit) * S.hw + hsub;
+        pk += kKeys * S.kw;
+    };
+    auto issue = [&](int stage) {
+        if (plive) {
+            const bool ok = pin && (unsigned)ppage < (unsigned)A.num_pages;
+            if (pin && !ok) atomicExch(&g_paged_error, (int)HGA_ERR_BOUNDS);
+            const int slot = ok ? (ppage << A.log2_page) + (ptok & page_mask) : -1;
+            const uint32_t bits = __ballot_sync(0xffffffffu, ok);
+            if (lane == 0) valid[warp][stage] = kKeys == 32 ? bits : bits & ((1u << (kKeys & 31)) - 1u);
+            const char *kb = static_cast<const char *>(A.k) + (int64_t)phead * D * sizeof(T);
+            const char *vb = static_cast<const char *>(A.v) + (int64_t)phead * D * sizeof(T);
+            const uint32_t dst = ring_s + stage * 2 * kTileBytes;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int row = (j * 32 + lane) / kCpr, ch = (j * 32 + lane) % kCpr;
+                const int sl = __shfl_sync(0xffffffffu, slot, row);
+                const int64_t off = (sl < 0 ? 0 : (int64_t)sl * row_bytes) + ch * 16;
+                const uint32_t to = dst + row * (kCpr * 16) + ((ch ^ (row & Tile::kSwz)) << 4);
+                cp16(to, kb + off, sl >= 0);
+                cp16(to + kTileBytes, vb + off, sl >= 0);
+            }
+            fetch();
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    // ---- consumer
+    Tile t;
+    int stage = 0;
+    int4 joined = make_int4(0, 0, -1, -1);
+    long long done = 0;                             // units before the segment
+    for (;;) {
+        const int k1 = C.k1(uk), hg = C.it / S.gsplit, g0 = (C.it % S.gsplit) * S.gch;
+        const int heads = min(S.gch, A.G - g0);
+        t.begin(A, C.b, (hg * S.hw + hsub) * A.G + g0, heads);
+        for (int k = C.k0(uk) + ksub * kKeys; k < k1; k += kKeys * S.kw) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncwarp();
+            issue(stage == 0 ? kStages - 1 : stage - 1);
+            const uint32_t ks = ring_s + stage * 2 * kTileBytes;
+            t.tile(ks, ks + kTileBytes, valid[warp][stage], A.scale_log2,
+                   ps + (sizeof(T) == 4 ? warp * kRows * kKeys : 0));
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+        }
+        t.end();
+        // ---- the segment's rows: merged over the warps of a head, then out or parked
+        const bool cont = C.u > 0, open = C.u + C.cnt < C.nu, whole = !cont && !open;
+        const int64_t row_at = ((int64_t)cta * 2 + (cont ? 0 : 1)) * S.rows;
+#pragma unroll
+        for (int round = 0; round < (kRows + Tile::kMerge - 1) / Tile::kMerge; ++round) {
+            t.put(round, merge + warp * Tile::kMerge * D, ml[warp]);
+            __syncthreads();
+            for (int e = tid; e < S.hw * Tile::kMerge * (D / 4); e += kThreads) {
+                const int d = (e % (D / 4)) * 4, r = e / (D / 4) % Tile::kMerge;
+                const int h = e / (D / 4 * Tile::kMerge), row = round * Tile::kMerge + r;
+                if (row >= heads) continue;
+                float top = -INFINITY;
+                for (int k = 0; k < S.kw; ++k) top = fmaxf(top, ml[k * S.hw + h][r].x);
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                float sum = 0.f;
+                const float ref = top == -INFINITY ? 0.f : top;
+                for (int k = 0; k < S.kw; ++k) {
+                    const int w = k * S.hw + h;
+                    const float f = ex2(ml[w][r].x - ref);
+                    const float4 x =
+                        *reinterpret_cast<const float4 *>(merge + (w * Tile::kMerge + r) * D + d);
+                    sum = fmaf(ml[w][r].y, f, sum);
+                    a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
+                    a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+                }
+                if (whole) {
+                    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+                    const int64_t at = (int64_t)C.b * A.Hq + (hg * S.hw + h) * A.G + g0 + row;
+                    put4<T>(static_cast<T *>(A.out) + at * D + d,
+                            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+                    if (A.lse && d == 0) A.lse[at] = (top + log2f(sum)) * kLn2;
+                } else {
+                    const int64_t at = row_at + h * S.gch + row;
+                    *reinterpret_cast<float4 *>(S.part + at * D + d) = a;
+                    if (d == 0) S.ml[at] = make_float2(top, sum);
+                }
+            }
+            __syncthreads();
+        }
+        if (!cont) {
+            if (open) {
+                // the CTA that holds the item's last unit
+                const long long last = u0 + done + C.nu - 1;
+                joined = make_int4(C.b, C.it, cta, (int)(((last + 1) * n - 1) / U));
+            }
+            if (S.by_item && tid == 0) S.join[(int64_t)C.b * S.items + C.it] = joined;
+        }
+        done += C.cnt;
+        if (!C.next(A, S, uk)) break;
+    }
+    if (!S.by_item && tid == 0) S.join[cta] = joined;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Adds up the parts of the items that were split, in CTA order.  One CTA per
+// possible split item and row; a programmatic dependent of k_paged_decode.
+constexpr int kJoinThreads = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs A, const Split S) {
+    constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
+    __shared__ float2 w[kMaxCtas];
+    __shared__ float red[kJoinThreads / 32];
+    __shared__ float4 acc[kGroups][kLanes];
+    __shared__ float sum_s;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 j = S.join[blockIdx.x];
+    if (j.z < 0) return;
+    const int row = blockIdx.y, h = row / S.gch, g = row % S.gch;
+    const int b = j.x, it = j.y;
+    const int g0 = (it % S.gsplit) * S.gch;
+    if (g0 + g >= A.G) return;
+    const int tid = threadIdx.x, cnt = j.w - j.z + 1;
+    float top = -INFINITY;
+    for (int i = tid; i < cnt; i += kJoinThreads) {
+        const float2 x = S.ml[((int64_t)(j.z + i) * 2 + (i == 0)) * S.rows + row];
+        w[i] = x;
+        top = fmaxf(top, x.x);
+    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((tid & 31) == 0) red[tid >> 5] = top;
+    __syncthreads();
+    for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, red[i]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int i = tid; i < cnt; i += kJoinThreads) w[i].x = ex2(w[i].x - ref);
+    __syncthreads();
+    if (tid < 32) {
+        float s = 0.f;
+        for (int i = tid; i < cnt; i += 32) s = fmaf(w[i].y, w[i].x, s);
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (tid == 0) sum_s = s;
+    }
+    const int lane = tid % kLanes, grp = tid / kLanes;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = grp; i < cnt; i += kGroups) {
+        const float4 x = *reinterpret_cast<const float4 *>(
+            S.part + (((int64_t)(j.z + i) * 2 + (i == 0)) * S.rows + row) * D + lane * 4);
+        const float f = w[i].x;
+        a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
+        a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
+    }
+    acc[grp][lane] = a;
+    __syncthreads();
+    if (grp) return;
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 x = acc[i][lane];
+        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+    }
+    const float sum = sum_s, inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+    const int64_t at = (int64_t)b * A.Hq + ((it / S.gsplit) * S.hw + h) * A.G + g0 + g;
+    put4<T>(static_cast<T *>(A.out) + at * D + lane * 4,
+            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+    if (A.lse && lane == 0) A.lse[at] = (top + log2f(sum)) * kLn2;
+}
+
+Split make_split(int B, int Hq, int Hkv, int dtype) {
+    Split S = {};
+    const int G = Hq / Hkv, most = dtype == HGA_BF16 ? 16 : 8;
+    S.hw = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
+    S.kw = kWarps / S.hw;
+    S.gsplit = (G + most - 1) / most;
+    S.gch = (G + S.gsplit - 1) / S.gsplit;
+    S.gsplit = (G + S.gch - 1) / S.gch;
+    S.items = Hkv / S.hw * S.gsplit;
+    S.rows = S.hw * S.gch;
+    S.by_item = (long long)B * S.items <= kMaxCtas;
+    return S;
+}
+
+inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <typename Tile, int D, int kRows>
+hga_status run(const PagedArgs &A, const Split &S, cudaStream_t st) {
+    auto *k = k_paged_decode<Tile, D, kRows>;
+    const size_t smem = smem_bytes<Tile, D>();
+    cudaError_t e = ensure_smem((const void *)k, smem);
+    if (e != cudaSuccess) return cuda_status(e);
+    k<<<S.n, kThreads, smem, st>>>(A, S);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
+    const int entries = S.by_item ? A.B * S.items : S.n;
+    return cuda_status(launch_dependent(k_paged_join<typename Tile::T, D>, dim3(entries, S.rows),
+                                        dim3(kJoinThreads), 0, st, A, S));
+}
+
+}  // namespace
+
+size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int dtype) {
+    const Split S = make_split(B, Hq, Hkv, dtype);
+    const size_t rows = (size_t)kMaxCtas * 2 * S.rows;
+    return up256(rows * D * 4) + up256(rows * sizeof(float2)) + up256(kMaxCtas * sizeof(int4));
+}
+
+hga_status launch_paged_decode(const PagedArgs &A, int dtype, int D, void *ws, cudaStream_t st) {
+    Split S = make_split(A.B, A.Hq, A.Hkv, dtype);
+    const size_t rows = (size_t)kMaxCtas * 2 * S.rows;
+    char *p = static_cast<char *>(ws);
+    S.part = reinterpret_cast<float *>(p);
+    p += up256(rows * D * 4);
+    S.ml = reinterpret_cast<float2 *>(p);
+    p += up256(rows * sizeof(float2));
+    S.join = reinterpret_cast<int4 *>(p);
+    // no more CTAs than there can be units: the longest row a sequence may have
+    long long most = (long long)A.max_pages << A.log2_page;
+    if (A.window > 0) most = std::min(most, (long long)A.window + A.sinks);
+    const int uk = kUnitTiles * (kTileBytes / (D * (dtype == HGA_BF16 ? 2 : 4)));
+    const long long units = (most + uk - 1) / uk * S.items * A.B;
+    S.n = (int)std::max(1ll, std::min(units, (long long)std::min(2 * sm_count(), kMaxCtas)));
+    if (dtype == HGA_BF16) {
+        if (D == 128)
+            return S.gch > 8 ? run<TileBf16<128, 16>, 128, 16>(A, S, st)
+                             : run<TileBf16<128, 8>, 128, 8>(A, S, st);
+        return S.gch > 8 ? run<TileBf16<64, 16>, 64, 16>(A, S, st)
+                         : run<TileBf16<64, 8>, 64, 8>(A, S, st);
+    }
+    if (D == 128)
+        return S.gch > 4 ? run<TileF32<128, 8>, 128, 8>(A, S, st)
+                         : run<TileF32<128, 4>, 128, 4>(A, S, st);
+    return S.gch > 4 ? run<TileF32<64, 8>, 64, 8>(A, S, st)
+                     : run<TileF32<64, 4>, 64, 4>(A, S, st);
+}
+
+hga_status paged_error_take(cudaStream_t st, bool clear) {
+    return take_error_word(g_paged_error, st, clear);
+}
+
+}  // namespace hga

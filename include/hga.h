@@ -343,6 +343,172 @@ typedef struct hga_hostkv_plan {
 hga_status hga_hostkv_plan_for(const hga_dims *dims, const hga_params *prm,
                                size_t workspace_bytes, hga_hostkv_plan *plan);
 
+/* ---------------------------------------------------------- paged cache --
+ *
+ * Layers that attend over every cached token, or over a token window, keep
+ * their keys and values in pages: a pool of num_pages pages of page_size
+ * tokens, [num_pages, page_size, Hkv, D] for the rotated keys and the same for
+ * the values, and a block table [B, max_pages] whose entry j is the page that
+ * holds the tokens j*page_size .. of sequence b.  The slot of a token is its
+ * page * page_size + its place in the page.  hga_paged_plan builds the table
+ * and the slots of a step, hga_qk_norm_rope writes keys and values through the
+ * slots, hga_paged_decode attends over the table.  Nothing here reads a length
+ * on the host, so a serving step can be captured in a CUDA graph.
+ *
+ * Limits: page_size a power of two; num_pages * page_size, max_pages *
+ * page_size and B * max_pages below 2^31; B and Hkv at most 65535; D 64 or 128.
+ * int32 buffers need 4-byte alignment, rows of q, k, v, pages and gradients
+ * 16-byte alignment.  Outputs must not overlap inputs except where stated. */
+typedef struct hga_paged_dims {
+    int32_t B;          /* sequences: rows of the block table, of lens and of q */
+    int32_t Hq, Hkv, D; /* as in hga_dims                                       */
+    int32_t dtype;      /* hga_dtype of q, pages and out                        */
+    int32_t num_pages;  /* pages in the pool                                    */
+    int32_t page_size;  /* tokens per page                                      */
+    int32_t max_pages;  /* columns of the block table                           */
+} hga_paged_dims;
+
+/* One step's plan.  All device pointers. */
+typedef struct hga_paged_plan_io {
+    const int32_t *lens;        /* [B] tokens each sequence holds               */
+    const int32_t *new_tokens;  /* [B] tokens this step adds, >= 0              */
+    const int32_t *release;     /* [B] or NULL: nonzero empties the row first   */
+    int32_t *free_pages;        /* [num_pages] stack of free page ids           */
+    const int32_t *free_count;  /* [1] entries on the stack; the top is the last */
+    int32_t *block_table;       /* [B, max_pages], new pages written in place   */
+    int32_t *lens_out;          /* [B] lens + granted; may be lens              */
+    int32_t *free_count_out;    /* [1]; may be free_count                       */
+    int32_t *cu_tokens;         /* [B + 1] exclusive sums of new_tokens         */
+    int32_t *granted;           /* [B] new_tokens[b], or 0 if refused           */
+    int32_t *slot;              /* [n_slots] slot of every packed new token     */
+    int32_t *pos;               /* [n_slots] its index in its sequence          */
+} hga_paged_plan_io;
+
+/* Block table, slot map and positions of one step, from the lengths alone.
+ * Rows with release[b] != 0 give their pages back first (rows in order, their
+ * pages in order) and count as empty.  Sequence b then needs
+ * ceil((lens+new)/page_size) - ceil(lens/page_size) pages; sequences are served
+ * in order, and page i of b's is the i-th from the top of what the sequences
+ * before it left.  A sequence is refused (granted 0, its length and row left as
+ * they are, its tokens' slots -1) when lens+new exceeds max_pages * page_size,
+ * when its packed tokens end beyond n_slots, or when it needs pages and the
+ * demand up to and including it exceeds the stack; one that needs no page is
+ * never refused for want of pages.  Packed token t of sequence b
+ * (cu_tokens[b] <= t < cu_tokens[b+1]) has position lens + t - cu_tokens[b];
+ * entries from cu_tokens[B] to n_slots get slot -1 and position 0, so a step of
+ * fewer tokens can replay a graph of n_slots.  Of dims, B, num_pages, page_size
+ * and max_pages are read.
+ * A negative length or count, a length beyond the row, a stack size outside
+ * [0, num_pages], a page id outside [0, num_pages) and a release that would
+ * overfill the stack are refused by the kernel: the row or the entry is left
+ * out and hga_device_status reports HGA_ERR_BOUNDS.
+ * workspace: hga_paged_plan_workspace(B, n_slots) bytes, 256-byte aligned; it
+ * needs no initial value. */
+hga_status hga_paged_plan(const hga_paged_dims *dims, const hga_paged_plan_io *io, int32_t n_slots,
+                          void *workspace, size_t workspace_bytes, void *stream);
+size_t hga_paged_plan_workspace(int32_t B, int32_t n_slots);
+
+typedef enum hga_rope_layout { HGA_ROPE_HALF = 0, HGA_ROPE_INTERLEAVED = 1 } hga_rope_layout;
+typedef enum hga_rope_scaling {
+    HGA_ROPE_UNSCALED = 0, HGA_ROPE_LINEAR = 1, HGA_ROPE_YARN = 2
+} hga_rope_scaling;
+
+/* A position rotation.  Pair i < R/2 of the first R = rotary_dim dimensions is
+ * (i, i + R/2) in the half layout and (2i, 2i + 1) in the interleaved one, and
+ * turns by p * w_i; dimensions R.. pass through.  w_i = theta^(-2i/R), and
+ *  LINEAR: w_i / factor;
+ *  YARN:   w_i (1 - g_i) + w_i / factor * g_i with g_i = clamp((i - lo) /
+ *          (hi - lo), 0, 1), lo = max(0, floor(d(beta_fast))), hi =
+ *          min(R - 1, ceil(d(beta_slow))) (hi = lo + 0.001 if equal), d(t) =
+ *          R ln(original_len / (2 pi t)) / (2 ln theta): pairs that turn more
+ *          than beta_fast times over the original length keep their rate.
+ * The rotated part is multiplied by `magnitude`; 0 selects 1, for YARN
+ * 0.1 ln(factor) + 1. */
+typedef struct hga_rope {
+    int32_t layout;        /* hga_rope_layout                                    */
+    int32_t rotary_dim;    /* R: a multiple of 16 up to D; 0 = no rotation       */
+    int32_t scaling;       /* hga_rope_scaling                                   */
+    int32_t original_len;  /* YARN: the trained length                           */
+    double theta, factor, beta_fast, beta_slow, magnitude;
+} hga_rope;
+
+/* Inputs and outputs of hga_qk_norm_rope.  q, k, v are [tokens, H, D] with the
+ * heads of a token D apart and tokens *_stride elements apart (a multiple of 16
+ * bytes, at least H*D), so views of a fused QKV buffer are read as they are. */
+typedef struct hga_qk_io {
+    const void *q, *k, *v;             /* raw projections; v may be NULL          */
+    int64_t q_stride, k_stride, v_stride;
+    const void *q_weight, *k_weight;   /* [D] norm weights; NULL: not normalised  */
+    double eps;                        /* of the norms, >= 0                      */
+    const int32_t *pos;                /* [tokens]; may be NULL if rotary_dim == 0 */
+    void *q_out, *k_out, *v_out;       /* dense [tokens, H, D]; each may be NULL   */
+    const int32_t *slot;               /* [tokens], with k_pages and v_pages       */
+    void *k_pages, *v_pages;           /* [num_pages, page_size, Hkv, D] or NULL   */
+    int64_t num_slots;                 /* num_pages * page_size                    */
+} hga_qk_io;
+
+/* Per-head RMS norms of queries and keys and the position rotation, in one pass
+ * over the projections: y = R_p (x (mean x^2 + eps)^(-1/2) weight), computed in
+ * fp32 and rounded once.  dims.B * dims.T tokens (dims.T may be any count).
+ * With rotary_dim == 0 the outputs are what hga_forward takes as raw q, k and v;
+ * rotated keys and values go to k_pages and v_pages at slot[t] for
+ * hga_paged_decode.  A slot of -1 writes no page row; any other slot outside
+ * [0, num_slots) writes none and hga_device_status reports HGA_ERR_BOUNDS.  The
+ * slots of one call must differ from one another.  Rows of the dense outputs are
+ * written for every token. */
+hga_status hga_qk_norm_rope(const hga_dims *dims, const hga_rope *rope, const hga_qk_io *io,
+                            void *stream);
+
+/* Inputs and outputs of hga_qk_norm_rope_backward. */
+typedef struct hga_qk_grad_io {
+    const void *q, *k;                 /* the forward's raw inputs (unused rows
+                                          may be NULL with weights NULL)         */
+    int64_t q_stride, k_stride;
+    const void *q_weight, *k_weight;   /* as in the forward                       */
+    double eps;
+    const int32_t *pos;
+    const void *d_q, *d_k, *d_v;       /* dense gradients of the dense outputs;
+                                          d_v may be NULL                         */
+    int32_t grad_dtype;                /* of d_q, d_k, d_v: HGA_F32 or dims.dtype */
+    void *dq, *dk, *dv;                /* [tokens, H, D] in dims.dtype, strided;
+                                          dv NULL exactly when d_v is             */
+    int64_t dq_stride, dk_stride, dv_stride;
+    float *d_q_weight, *d_k_weight;    /* [D], required exactly with the weights  */
+} hga_qk_grad_io;
+
+/* Gradients of hga_qk_norm_rope.  With g = R_p^T dy, r = (mean x^2 + eps)^(-1/2):
+ *   d_weight_d = sum over tokens and heads of g_d x_d r
+ *   dx = r (g w - x r^2 mean_d(g w x))      (g itself where not normalised)
+ * and dv = d_v.  d_q, d_k, d_v may be the fp32 gradients of hga_attend_backward.
+ * Sums are formed in a fixed order: the same inputs give the same bits.
+ * workspace: hga_qk_norm_rope_backward_workspace(dims) bytes, 256-byte aligned;
+ * it needs no initial value. */
+hga_status hga_qk_norm_rope_backward(const hga_dims *dims, const hga_rope *rope,
+                                     const hga_qk_grad_io *io, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+size_t hga_qk_norm_rope_backward_workspace(const hga_dims *dims);
+
+/* Attention of one new token per sequence over its pages.  q [B, Hq, D] is
+ * rotated; sequence b attends, with `scale` (0 selects 1/sqrt(D)), to its tokens
+ * j < lens[b], its own included; with window > 0 only to those with
+ * j >= lens[b] - window or j < sinks.  out [B, Hq, D]; lse [B, Hq] f32 may be
+ * NULL.  A sequence of length 0 gives zeros and an lse of -inf.  Pages that hold
+ * no attended token are not read, and neither is what a last page holds behind
+ * the length.  A length outside [0, max_pages * page_size] counts as 0, the keys
+ * of a page id outside [0, num_pages) are left out, and hga_device_status
+ * reports HGA_ERR_BOUNDS.
+ * The work is split over sequences, heads and length by the lengths on the
+ * device; partial results are joined in a fixed order, so the same inputs give
+ * the same bits.  fp32 softmax statistics and sums; for bf16 the softmax weights
+ * are rounded to bf16 for their product with the values.
+ * workspace: hga_paged_decode_workspace(dims) bytes, 256-byte aligned; it needs
+ * no initial value.  Calls that share a workspace must not overlap on the GPU. */
+hga_status hga_paged_decode(const hga_paged_dims *dims, const void *q, const void *k_pages,
+                            const void *v_pages, const int32_t *block_table, const int32_t *lens,
+                            int32_t window, int32_t sinks, double scale, void *out, float *lse,
+                            void *workspace, size_t workspace_bytes, void *stream);
+size_t hga_paged_decode_workspace(const hga_paged_dims *dims);
+
 /* Status recorded by the kernels themselves since the last reset: a bounded
  * wait that gave up (HGA_ERR_TIMEOUT: the kernel recorded it, released what
  * it held and returned without finishing its tile) or a device-side index

@@ -1,0 +1,248 @@
+"""The paged-cache operators' argument checks: refused on the host, before
+anything is launched (the fake pointers below are never dereferenced, and no call
+here is valid enough to launch), and the reference's own pins."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import hierarchical_kv_routing_b200 as hga
+from hierarchical_kv_routing_b200 import _build, paged
+from tests import paged_reference as ref
+
+A = 1 << 24
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 6
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return hga.load()
+
+
+def pdims(**kw):
+    d = dict(B=4, Hq=8, Hkv=2, D=64, dtype=1, num_pages=100, page_size=16, max_pages=10)
+    d.update(kw)
+    return paged._PagedDims(**d)
+
+
+BAD_PAGES = [(dict(B=0), INVALID), (dict(num_pages=0), INVALID), (dict(page_size=0), INVALID),
+             (dict(page_size=-16), INVALID), (dict(max_pages=0), INVALID), (dict(page_size=24), UNSUPPORTED),
+             (dict(B=65536), UNSUPPORTED), (dict(num_pages=1 << 27), UNSUPPORTED),
+             (dict(max_pages=1 << 27), UNSUPPORTED), (dict(B=60000, max_pages=60000), UNSUPPORTED)]
+BAD_HEADS = [(dict(Hq=0), INVALID), (dict(Hkv=3), INVALID), (dict(D=96), UNSUPPORTED),
+             (dict(dtype=2), INVALID), (dict(Hq=1 << 17, Hkv=1), UNSUPPORTED)]
+
+
+def plan_io(**kw):
+    d = {n: A for n, _ in paged._PlanIO._fields_}
+    d.update(kw)
+    return paged._PlanIO(**d)
+
+
+def call_plan(lib, d, io, n=8, ws=A, nbytes=1 << 20):
+    return lib.hga_paged_plan(ctypes.byref(d), ctypes.byref(io), n, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("bad,code", BAD_PAGES)
+def test_plan_dims(lib, bad, code):
+    assert call_plan(lib, pdims(**bad), plan_io()) == code
+
+
+def test_plan_pointers_and_workspace(lib):
+    for f in ("lens", "new_tokens", "free_pages", "free_count", "block_table", "lens_out",
+              "free_count_out", "cu_tokens", "granted", "slot", "pos"):
+        assert call_plan(lib, pdims(), plan_io(**{f: None})) == INVALID, f
+    for f, _ in paged._PlanIO._fields_:
+        assert call_plan(lib, pdims(), plan_io(**{f: A + 2})) == INVALID, f
+    assert call_plan(lib, pdims(), plan_io(), n=-1) == INVALID
+    assert lib.hga_paged_plan(None, None, 0, None, 0, None) == INVALID
+    need = lib.hga_paged_plan_workspace(4, 8)
+    assert need >= 16
+    assert call_plan(lib, pdims(), plan_io(), nbytes=need - 1) == WORKSPACE
+    assert call_plan(lib, pdims(), plan_io(), ws=None) == WORKSPACE
+    assert call_plan(lib, pdims(), plan_io(), ws=A + 16) == WORKSPACE
+    assert lib.hga_paged_plan_workspace(0, 8) == 0 and lib.hga_paged_plan_workspace(4, -1) == 0
+
+
+def decode_call(lib, d, **kw):
+    a = dict(q=A, k=A, v=A, table=A, lens=A, window=0, sinks=0, scale=0.0, out=A, lse=None, ws=A,
+             nbytes=1 << 28)
+    a.update(kw)
+    return lib.hga_paged_decode(ctypes.byref(d), a["q"], a["k"], a["v"], a["table"], a["lens"],
+                                a["window"], a["sinks"], a["scale"], a["out"], a["lse"], a["ws"],
+                                a["nbytes"], None)
+
+
+@pytest.mark.parametrize("bad,code", BAD_PAGES + BAD_HEADS)
+def test_decode_dims(lib, bad, code):
+    assert decode_call(lib, pdims(**bad)) == code
+    assert lib.hga_paged_decode_workspace(ctypes.byref(pdims(**bad))) == 0
+
+
+def test_decode_pointers_values_and_workspace(lib):
+    for f in ("q", "k", "v", "table", "lens", "out"):
+        assert decode_call(lib, pdims(), **{f: None}) == INVALID
+    for f in ("q", "k", "v", "out"):
+        assert decode_call(lib, pdims(), **{f: A + 8}) == INVALID
+    for f in ("table", "lens", "lse"):
+        assert decode_call(lib, pdims(), **{f: A + 2}) == INVALID
+    for kw in (dict(window=-1), dict(sinks=-1), dict(scale=-1.0), dict(scale=float("nan")),
+               dict(scale=float("inf"))):
+        assert decode_call(lib, pdims(), **kw) == INVALID
+    need = lib.hga_paged_decode_workspace(ctypes.byref(pdims()))
+    assert need > 0
+    assert decode_call(lib, pdims(), nbytes=need - 1) == WORKSPACE
+    assert decode_call(lib, pdims(), ws=None) == WORKSPACE
+    assert decode_call(lib, pdims(), ws=A + 128) == WORKSPACE
+
+
+def tdims(**kw):
+    d = dict(B=1, T=7, Hq=4, Hkv=2, D=64, dtype=1)
+    d.update(kw)
+    return paged._TokenDims(**d)
+
+
+def qk_io(**kw):
+    d = dict(q=A, k=A, v=A, q_stride=512, k_stride=512, v_stride=512, q_weight=A, k_weight=A, eps=1e-6,
+             pos=A, q_out=A, k_out=A, v_out=A)
+    d.update(kw)
+    return paged._QkIO(**d)
+
+
+def grad_io(**kw):
+    d = {n: A for n in ("q", "k", "q_weight", "k_weight", "pos", "d_q", "d_k", "d_v", "dq", "dk", "dv",
+                        "d_q_weight", "d_k_weight")}
+    d.update({n: 512 for n in ("q_stride", "k_stride", "dq_stride", "dk_stride", "dv_stride")})
+    d.update(eps=1e-6, grad_dtype=1)
+    d.update(kw)
+    return paged._QkGradIO(**d)
+
+
+def call_qk(lib, d, io, rope=None):
+    r = rope or hga.HGARope().c(64)
+    return lib.hga_qk_norm_rope(ctypes.byref(d), ctypes.byref(r), ctypes.byref(io), None)
+
+
+def call_grad(lib, d, io, rope=None, ws=A, nbytes=1 << 24):
+    r = rope or hga.HGARope().c(64)
+    return lib.hga_qk_norm_rope_backward(ctypes.byref(d), ctypes.byref(r), ctypes.byref(io), ws, nbytes,
+                                         None)
+
+
+@pytest.mark.parametrize("bad,code", BAD_HEADS + [(dict(B=0), INVALID), (dict(T=-1), INVALID),
+                                                  (dict(B=1 << 16, T=1 << 16), UNSUPPORTED)])
+def test_qk_dims(lib, bad, code):
+    assert call_qk(lib, tdims(**bad), qk_io()) == code
+    assert call_grad(lib, tdims(**bad), grad_io()) == code
+    assert lib.hga_qk_norm_rope_backward_workspace(ctypes.byref(tdims(**bad))) == 0
+
+
+@pytest.mark.parametrize("bad,code", [
+    (dict(rotary_dim=80), INVALID), (dict(rotary_dim=-16), INVALID), (dict(rotary_dim=24), UNSUPPORTED),
+    (dict(theta=1.0), INVALID), (dict(theta=float("nan")), INVALID), (dict(theta=float("inf")), INVALID),
+    (dict(scaling="linear", factor=0.5), INVALID), (dict(scaling="linear", factor=float("inf")), INVALID),
+    (dict(scaling="yarn", factor=2.0), INVALID),
+    (dict(scaling="yarn", factor=2.0, original_len=64, beta_slow=0.0), INVALID),
+    (dict(scaling="yarn", factor=2.0, original_len=64, beta_slow=33.0), INVALID),
+    (dict(magnitude=-1.0), INVALID), (dict(magnitude=float("nan")), INVALID)])
+def test_rope_values(lib, bad, code):
+    r = hga.HGARope(**bad).c(64)
+    assert call_qk(lib, tdims(), qk_io(), r) == code
+    assert call_grad(lib, tdims(), grad_io(), r) == code
+    for field, value in (("layout", 2), ("layout", -1), ("scaling", 3)):
+        r = hga.HGARope().c(64)
+        setattr(r, field, value)
+        assert call_qk(lib, tdims(), qk_io(), r) == INVALID
+
+
+def test_rope_names():
+    for kw in (dict(layout="neox"), dict(scaling="ntk")):
+        with pytest.raises(hga.HGAError):
+            hga.HGARope(**kw).c(64)
+
+
+def test_qk_pointers_and_strides(lib):
+    for f in ("q", "k", "v", "pos"):
+        assert call_qk(lib, tdims(), qk_io(**{f: None})) == INVALID, f
+    for f in ("q", "k", "v", "q_out", "k_out", "v_out", "q_weight", "k_weight"):
+        assert call_qk(lib, tdims(), qk_io(**{f: A + 8})) == INVALID, f
+    for f, v in (("q_stride", 255), ("q_stride", 260), ("k_stride", 127), ("v_stride", 0),
+                 ("v_stride", 1 << 50), ("q_stride", -512)):
+        assert call_qk(lib, tdims(), qk_io(**{f: v})) == INVALID, f
+    for eps in (-1e-6, float("nan"), float("inf")):
+        assert call_qk(lib, tdims(), qk_io(eps=eps)) == INVALID
+        assert call_grad(lib, tdims(), grad_io(eps=eps)) == INVALID
+    for kw in (dict(k_pages=A), dict(k_pages=A, slot=A), dict(k_pages=A, slot=A + 2, num_slots=8),
+               dict(v_pages=A, num_slots=8), dict(k_pages=A + 4, slot=A, num_slots=8)):
+        assert call_qk(lib, tdims(), qk_io(**kw)) == INVALID
+    assert call_qk(lib, tdims(), qk_io(k_pages=A, slot=A, num_slots=1 << 31)) == UNSUPPORTED
+
+
+def test_qk_grad_pointers_and_workspace(lib):
+    for f in ("q", "k", "pos", "d_q", "d_k", "dq", "dk", "d_v", "dv", "q_weight", "d_q_weight",
+              "k_weight", "d_k_weight"):
+        assert call_grad(lib, tdims(), grad_io(**{f: None})) == INVALID, f
+    for f in ("q", "k", "d_q", "d_k", "d_v", "dq", "dk", "dv", "q_weight", "k_weight"):
+        assert call_grad(lib, tdims(), grad_io(**{f: A + 8})) == INVALID, f
+    for f in ("d_q_weight", "d_k_weight", "pos"):
+        assert call_grad(lib, tdims(), grad_io(**{f: A + 2})) == INVALID, f
+    for f in ("q_stride", "k_stride", "dq_stride", "dk_stride", "dv_stride"):
+        assert call_grad(lib, tdims(), grad_io(**{f: 4})) == INVALID, f
+    assert call_grad(lib, tdims(dtype=0), grad_io(grad_dtype=1)) == INVALID
+    assert call_grad(lib, tdims(), grad_io(grad_dtype=2)) == INVALID
+    need = lib.hga_qk_norm_rope_backward_workspace(ctypes.byref(tdims()))
+    assert need > 0
+    assert call_grad(lib, tdims(), grad_io(), nbytes=need - 1) == WORKSPACE
+    assert call_grad(lib, tdims(), grad_io(), ws=None) == WORKSPACE
+    assert call_grad(lib, tdims(), grad_io(), ws=A + 64) == WORKSPACE
+
+
+def test_binding_refuses_cpu_tensors():
+    i = torch.zeros(2, dtype=torch.int32)
+    x = torch.zeros(2, 2, 64)
+    with pytest.raises(hga.HGAError):
+        hga.hga_paged_plan(i, i, i, i[:1], torch.zeros(2, 3, dtype=torch.int32), 16, 4)
+    with pytest.raises(hga.HGAError):
+        hga.hga_qk_norm_rope(x, x, x, i, hga.HGARope())
+    with pytest.raises(hga.HGAError):
+        hga.hga_qk_norm_rope_backward(x, x, x, x, i, hga.HGARope())
+    with pytest.raises(hga.HGAError):
+        hga.hga_paged_decode(x, x[None], x[None], torch.zeros(2, 3, dtype=torch.int32), i)
+    with pytest.raises(hga.HGAError):
+        paged._count(1 << 31, "window")
+
+
+def test_reference_plan_pins():
+    """By hand: two rows, pages of 4, a stack of three."""
+    r = ref.plan([3, 4], [2, 1], [7, 8, 9], 3, [[0, -1, -1], [1, -1, -1]], 4, 4)
+    assert r["cu_tokens"] == [0, 2, 3] and r["granted"] == [2, 1] and r["lens"] == [5, 5]
+    assert r["table"] == [[0, 9, -1], [1, 8, -1]] and r["free_count"] == [1]
+    assert r["slot"] == [3, 36, 32, -1] and r["pos"] == [3, 4, 4, 0]
+    r = ref.plan([4, 4, 1], [1, 1, 1], [9, 0, 0], 1, [[0, -1], [1, -1], [2, -1]], 4, 3)
+    assert r["granted"] == [1, 0, 1] and r["slot"] == [36, -1, 9]      # the page goes to the first
+    r = ref.plan([5, 1], [0, 9], [3, 0, 0, 0, 0], 1, [[0, 1, -1], [2, -1, -1]], 4, 9, [1, 0])
+    assert r["free"][:3] == [3, 0, 1] and r["lens"] == [0, 10] and r["table"][1] == [2, 1, 0]
+
+
+def test_reference_rotation_pins():
+    """Complex rotation for both layouts; the transpose undoes it; attention over a
+    window that covers everything is attention over everything."""
+    rng = np.random.default_rng(0)
+    x, pos = rng.normal(size=(5, 2, 64)), np.arange(5) * 7
+    for layout in ("half", "interleaved"):
+        for R in (0, 16, 48, 64):
+            w = ref.rates(R, 1e4)
+            y = ref.rotate(x, pos, R, layout, w, 1.0)
+            a, b = ref.members(R, layout)
+            z = (x[..., a] + 1j * x[..., b]) * np.exp(1j * pos[:, None, None] * w)
+            assert np.allclose(y[..., a], z.real) and np.allclose(y[..., b], z.imag)
+            assert np.array_equal(y[..., R:], x[..., R:])
+            assert np.allclose(ref.rotate(y, pos, R, layout, w, 1.0, back=True), x)
+    w = ref.rates(64, 1e4, "yarn", 4.0, 4096)
+    base = ref.rates(64, 1e4)
+    assert np.allclose(w[0], base[0]) and np.allclose(w[-1], base[-1] / 4)
+    assert (np.diff(w / base) <= 1e-12).all()
+    assert ref.visible(9, 3, 2) == [0, 1, 6, 7, 8] and ref.visible(3, 9, 2) == [0, 1, 2]
+    assert ref.visible(4, 0, 2) == [0, 1, 2, 3]
