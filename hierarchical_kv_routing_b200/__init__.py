@@ -102,6 +102,8 @@ def lib_path() -> str:
 def load():
     """Load libhga.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -52,10 +52,9 @@ hga_status check_tokens(const hga_dims *d) {
     return (long long)d->B * d->T > INT_MAX ? HGA_ERR_UNSUPPORTED : HGA_OK;
 }
 
-hga_status make_rope(const hga_rope *r, int D, PairRope *out) {
+hga_status form_rope(const hga_rope *r, int D, PairRope *out) {
     std::memset(out, 0, sizeof(*out));
     out->magnitude = 1.f;
-    if (!r) return HGA_ERR_INVALID_ARG;
     if (r->layout != HGA_ROPE_HALF && r->layout != HGA_ROPE_INTERLEAVED) return HGA_ERR_INVALID_ARG;
     if (r->rotary_dim < 0 || r->rotary_dim > D) return HGA_ERR_INVALID_ARG;
     if (r->rotary_dim % 16) return HGA_ERR_UNSUPPORTED;
@@ -94,6 +93,24 @@ hga_status make_rope(const hga_rope *r, int D, PairRope *out) {
         out->turn[i] = (unsigned long long)llroundl((long double)w / two_pi * 18446744073709551616.0L);
     }
     out->magnitude = (float)(r->magnitude > 0.0 ? r->magnitude : magnitude);
+    return HGA_OK;
+}
+
+// The constants of a rotation, kept per thread for the one used last: R / 2 powers
+// and extended-precision products take longer than a small step's kernel.
+hga_status make_rope(const hga_rope *r, int D, PairRope *out) {
+    thread_local hga_rope last;
+    thread_local int last_D = 0;               // 0: nothing kept
+    thread_local PairRope kept;
+    if (!r) return HGA_ERR_INVALID_ARG;
+    if (last_D != D || std::memcmp(&last, r, sizeof(last))) {
+        last_D = 0;
+        const hga_status s = form_rope(r, D, &kept);
+        if (s != HGA_OK) return s;
+        last = *r;
+        last_D = D;
+    }
+    *out = kept;
     return HGA_OK;
 }
 

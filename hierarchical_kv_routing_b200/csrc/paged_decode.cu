@@ -26,10 +26,12 @@
 // A CTA is four warps that run on their own: each streams tiles of 4 KB of K and
 // 4 KB of V through a ring of kStages in shared memory (cp.async, 16 bytes a
 // lane), three deep, so two CTAs per SM keep 128 KB in flight, above the ~50 KB
-// that 7 TB/s and a microsecond of latency ask for.  The page of each key comes from the block table one tile
-// ahead of its loads.  Where Hkv allows, the four warps take the same keys of
-// adjacent heads (whole runs of a page's token rows) and never meet; else they
-// take every fourth tile of one head and are merged in shared memory.
+// that 7 TB/s and a microsecond of latency ask for.  The page of each key comes
+// from the block table one tile ahead of its loads.  The warps take every fourth
+// tile of one KV head and are merged in shared memory at an item's end.  (Giving
+// the four warps adjacent heads of the same keys instead, whole runs of a page's
+// token rows, costs four times the parts and was slower: 326 against 317 us at
+// 16 x 64K tokens of 4 heads of 128, 33 against 24 us at 1 x 32K.)
 #include <algorithm>
 
 #include "paged_internal.cuh"
@@ -46,14 +48,12 @@ constexpr int kMaxCtas = 2 * 148;            // two per SM
 constexpr int kUnitTiles = 4;                // tiles of a unit, over the warps of one head
 
 struct Split {
-    int items;         // per sequence: Hkv / hw * gsplit
-    int hw, kw;        // KV heads per CTA, warps per KV head (hw * kw = kWarps)
-    int gsplit, gch;   // chunks of a KV head's query heads, heads per chunk
-    int rows;          // hw * gch: rows of an item
+    int items;         // per sequence: Hkv * gsplit
+    int gsplit, gch;   // chunks of a KV head's query heads, heads (rows) per chunk
     int n;             // CTAs
     int by_item;       // join entries indexed by item (else by the CTA that starts it)
-    float *part;       // [n][2][rows][D]: continued and opened item, unnormalised
-    float2 *ml;        // [n][2][rows]: running maximum (base 2) and sum
+    float *part;       // [n][2][gch][D]: continued and opened item, unnormalised
+    float2 *ml;        // [n][2][gch]: running maximum (base 2) and sum
     int4 *join;        // entry: (sequence, item, first CTA, last CTA); first -1: not split
 };
 
@@ -434,17 +434,34 @@ template <> __device__ __forceinline__ void put4<__nv_bfloat16>(__nv_bfloat16 *p
 
 constexpr float kLn2 = 0.693147180559945f;
 
+// The rows of empty sequences, shared out over the CTAs; bad lengths are reported here.
+template <typename T, int D>
+__device__ __forceinline__ void empty_rows(const PagedArgs &A, const Split &S) {
+    for (int b = blockIdx.x; b < A.B; b += gridDim.x) {
+        if (visible(A, b).n) continue;
+        if (threadIdx.x == 0 && A.lens[b] != 0) atomicExch(&g_paged_error, (int)HGA_ERR_BOUNDS);
+        T *o = static_cast<T *>(A.out) + (int64_t)b * A.Hq * D;
+        for (int i = threadIdx.x; i < A.Hq * D / 4; i += kThreads)
+            put4<T>(o + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+        for (int h = threadIdx.x; A.lse && h < A.Hq; h += kThreads)
+            A.lse[(int64_t)b * A.Hq + h] = -INFINITY;
+        if (S.by_item)
+            for (int i = threadIdx.x; i < S.items; i += kThreads)
+                S.join[(int64_t)b * S.items + i] = make_int4(0, 0, -1, -1);
+    }
+}
+
 template <typename Tile, int D, int kRows>
 __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A, const Split S) {
     using T = typename Tile::T;
     constexpr int kKeys = Tile::kKeys, kCpr = D * (int)sizeof(T) / 16, kLoads = kTileBytes / 512;
     extern __shared__ __align__(1024) char ring[];
-    __shared__ int start[4];                       // b, item, unit of the CTA's first unit
+    __shared__ int start[3];                       // b, item, unit of the CTA's first unit
+    __shared__ long long sums[kWarps];
     __shared__ uint32_t valid[kWarps][kStages];
     __shared__ float2 ml[kWarps][Tile::kMerge];
     __shared__ __align__(16) float ps[sizeof(T) == 4 ? kWarps * kRows * kKeys : 1];
     float *merge = reinterpret_cast<float *>(ring + kWarps * kStages * 2 * kTileBytes);
-    long long *sums = reinterpret_cast<long long *>(ring);   // before the ring is in use
 
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
@@ -454,13 +471,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     const int r0 = min(A.B, tid * per), r1 = min(A.B, r0 + per);
     long long mine = 0;
     for (int b = r0; b < r1; ++b) mine += (long long)units_of(visible(A, b).n, uk) * S.items;
-    sums[tid] = mine;
-    if (tid < 4) start[tid] = -1;
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    long long before = 0, U = 0;
-    for (int t = 0; t < kThreads; ++t) {
-        if (t < tid) before += sums[t];
-        U += sums[t];
+    long long before = upto - mine, U = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sums[w];
+        U += sums[w];
     }
     // with fewer units than CTAs the last ones take none, so that a split item's
     // parts lie in CTAs without a gap
@@ -479,23 +502,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
             at -= (long long)nu * S.items;
         }
     }
-    // rows of empty sequences, shared out over the CTAs; bad lengths are reported here
-    for (int b = cta; b < A.B; b += gridDim.x) {
-        const Visible v = visible(A, b);
-        if (v.n) continue;
-        if (tid == 0 && A.lens[b] != 0) atomicExch(&g_paged_error, (int)HGA_ERR_BOUNDS);
-        T *o = static_cast<T *>(A.out) + (int64_t)b * A.Hq * D;
-        for (int i = tid; i < A.Hq * D / 4; i += kThreads)
-            put4<T>(o + i * 4, make_float4(0.f, 0.f, 0.f, 0.f));
-        for (int h = tid; A.lse && h < A.Hq; h += kThreads)
-            A.lse[(int64_t)b * A.Hq + h] = -INFINITY;
-        if (S.by_item)
-            for (int i = tid; i < S.items; i += kThreads)
-                S.join[(int64_t)b * S.items + i] = make_int4(0, 0, -1, -1);
-    }
     __syncthreads();
     if (u0 >= u1) {
         if (tid == 0 && !S.by_item) S.join[cta] = make_int4(0, 0, -1, -1);
+        empty_rows<T, D>(A, S);
         return;
     }
 
@@ -506,14 +516,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     C.nu = units_of(C.v.n, uk);
     C.take();
     Walk P = C;
-    const int hsub = warp % S.hw, ksub = warp / S.hw;
     char *kring = ring + warp * kStages * 2 * kTileBytes;
     const uint32_t ring_s = su32(kring);
     const int64_t row_bytes = (int64_t)A.Hkv * D * (int)sizeof(T);
     const int page_mask = (1 << A.log2_page) - 1;
 
     // ---- producer: the next tile's page entries are read one tile ahead of its rows
-    int pk = P.k0(uk) + ksub * kKeys, pk1 = P.k1(uk);
+    int pk = P.k0(uk) + warp * kKeys, pk1 = P.k1(uk);
     bool plive = true;                              // false: no tile left
     int ptok = 0, ppage = 0, phead = 0;
     bool pin = false;
@@ -523,15 +532,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
                 plive = false;
                 return;
             }
-            pk = P.k0(uk) + ksub * kKeys;
+            pk = P.k0(uk) + warp * kKeys;
             pk1 = P.k1(uk);
         }
         const int key = pk + (lane & (kKeys - 1));
         pin = key < pk1;
         ptok = key < P.v.s ? key : key - P.v.s + P.v.lo;
         ppage = pin ? A.table[(int64_t)P.b * A.max_pages + (ptok >> A.log2_page)] : 0;
-        phead = (P.it / S.gsplit) * S.hw + hsub;
-        pk += kKeys * S.kw;
+        phead = P.it / S.gsplit;
+        pk += kKeys * kWarps;
     };
     auto issue = [&](int stage) {
         if (plive) {
@@ -566,10 +575,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     int4 joined = make_int4(0, 0, -1, -1);
     long long done = 0;                             // units before the segment
     for (;;) {
-        const int k1 = C.k1(uk), hg = C.it / S.gsplit, g0 = (C.it % S.gsplit) * S.gch;
+        const int k1 = C.k1(uk), h = C.it / S.gsplit, g0 = (C.it % S.gsplit) * S.gch;
         const int heads = min(S.gch, A.G - g0);
-        t.begin(A, C.b, (hg * S.hw + hsub) * A.G + g0, heads);
-        for (int k = C.k0(uk) + ksub * kKeys; k < k1; k += kKeys * S.kw) {
+        t.begin(A, C.b, h * A.G + g0, heads);
+        for (int k = C.k0(uk) + warp * kKeys; k < k1; k += kKeys * kWarps) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
             __syncwarp();
             issue(stage == 0 ? kStages - 1 : stage - 1);
@@ -579,24 +588,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
             stage = stage == kStages - 1 ? 0 : stage + 1;
         }
         t.end();
-        // ---- the segment's rows: merged over the warps of a head, then out or parked
+        // ---- the segment's rows: merged over the warps, then out or parked
         const bool cont = C.u > 0, open = C.u + C.cnt < C.nu, whole = !cont && !open;
-        const int64_t row_at = ((int64_t)cta * 2 + (cont ? 0 : 1)) * S.rows;
+        const int64_t row_at = ((int64_t)cta * 2 + (cont ? 0 : 1)) * S.gch;
 #pragma unroll
         for (int round = 0; round < (kRows + Tile::kMerge - 1) / Tile::kMerge; ++round) {
             t.put(round, merge + warp * Tile::kMerge * D, ml[warp]);
             __syncthreads();
-            for (int e = tid; e < S.hw * Tile::kMerge * (D / 4); e += kThreads) {
-                const int d = (e % (D / 4)) * 4, r = e / (D / 4) % Tile::kMerge;
-                const int h = e / (D / 4 * Tile::kMerge), row = round * Tile::kMerge + r;
-                if (row >= heads) continue;
+            for (int e = tid; e < Tile::kMerge * (D / 4); e += kThreads) {
+                const int d = (e % (D / 4)) * 4, r = e / (D / 4), row = round * Tile::kMerge + r;
+                if (row >= heads) break;
                 float top = -INFINITY;
-                for (int k = 0; k < S.kw; ++k) top = fmaxf(top, ml[k * S.hw + h][r].x);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][r].x);
+                const float ref = top == -INFINITY ? 0.f : top;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
                 float sum = 0.f;
-                const float ref = top == -INFINITY ? 0.f : top;
-                for (int k = 0; k < S.kw; ++k) {
-                    const int w = k * S.hw + h;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
                     const float f = ex2(ml[w][r].x - ref);
                     const float4 x =
                         *reinterpret_cast<const float4 *>(merge + (w * Tile::kMerge + r) * D + d);
@@ -606,12 +615,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
                 }
                 if (whole) {
                     const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-                    const int64_t at = (int64_t)C.b * A.Hq + (hg * S.hw + h) * A.G + g0 + row;
+                    const int64_t at = (int64_t)C.b * A.Hq + h * A.G + g0 + row;
                     put4<T>(static_cast<T *>(A.out) + at * D + d,
                             make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
                     if (A.lse && d == 0) A.lse[at] = (top + log2f(sum)) * kLn2;
                 } else {
-                    const int64_t at = row_at + h * S.gch + row;
+                    const int64_t at = row_at + row;
                     *reinterpret_cast<float4 *>(S.part + at * D + d) = a;
                     if (d == 0) S.ml[at] = make_float2(top, sum);
                 }
@@ -631,11 +640,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     }
     if (!S.by_item && tid == 0) S.join[cta] = joined;
     asm volatile("cp.async.wait_all;" ::: "memory");
+    empty_rows<T, D>(A, S);
 }
 
-// Adds up the parts of the items that were split, in CTA order.  One CTA per
-// possible split item and row; a programmatic dependent of k_paged_decode.
-constexpr int kJoinThreads = 256;
+// Adds up the parts of the items that were split, in CTA order; a programmatic
+// dependent of k_paged_decode.  grid: (possible split items, rows).  Latency
+// bound: an item of up to kFew parts is joined by its first CTA, a group of D / 4
+// lanes per row and four parts loaded at a time; beyond that every row has its
+// CTA, whose groups share the parts.  (One CTA per row throughout: 12 us instead
+// of 4 for 384 items of 2 or 3 parts.)
+constexpr int kJoinThreads = 256, kAhead = 8, kFew = 16;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs A, const Split S) {
     constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
@@ -646,64 +660,114 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs A, 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 j = S.join[blockIdx.x];
     if (j.z < 0) return;
-    const int row = blockIdx.y, h = row / S.gch, g = row % S.gch;
-    const int b = j.x, it = j.y;
-    const int g0 = (it % S.gsplit) * S.gch;
-    if (g0 + g >= A.G) return;
-    const int tid = threadIdx.x, cnt = j.w - j.z + 1;
+    const int b = j.x, h = j.y / S.gsplit, g0 = (j.y % S.gsplit) * S.gch;
+    const int tid = threadIdx.x, cnt = j.w - j.z + 1, heads = min(S.gch, A.G - g0);
+    const int lane = tid % kLanes, grp = tid / kLanes;
+    auto out = [&](int row, float4 a, float top, float sum) {
+        const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+        const int64_t to = (int64_t)b * A.Hq + h * A.G + g0 + row;
+        put4<T>(static_cast<T *>(A.out) + to * D + lane * 4,
+                make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+        if (A.lse && lane == 0) A.lse[to] = (top + log2f(sum)) * kLn2;
+    };
+    if (cnt <= kFew) {
+        if (blockIdx.y) return;
+        for (int row = grp; row < heads; row += kGroups) {
+            float top = -INFINITY, sum = 0.f;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i0 = 0; i0 < cnt; i0 += 4) {
+                float4 x[4];
+                float2 y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = i0 + k;
+                    const int64_t at = ((int64_t)(j.z + i) * 2 + (i == 0)) * S.gch + row;
+                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    y[k] = make_float2(-INFINITY, 0.f);
+                    if (i < cnt) {
+                        x[k] = *reinterpret_cast<const float4 *>(S.part + at * D + lane * 4);
+                        y[k] = S.ml[at];
+                    }
+                }
+                const float up = fmaxf(fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x)), top);
+                const float ref = up == -INFINITY ? 0.f : up, f0 = ex2(top - ref);
+                top = up;
+                sum *= f0;
+                a.x *= f0, a.y *= f0, a.z *= f0, a.w *= f0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float f = ex2(y[k].x - ref);
+                    sum = fmaf(y[k].y, f, sum);
+                    a.x = fmaf(x[k].x, f, a.x), a.y = fmaf(x[k].y, f, a.y);
+                    a.z = fmaf(x[k].z, f, a.z), a.w = fmaf(x[k].w, f, a.w);
+                }
+            }
+            out(row, a, top, sum);
+        }
+        return;
+    }
+    const int row = blockIdx.y;
+    if (row >= heads) return;
+    auto at = [&](int i) { return ((int64_t)(j.z + i) * 2 + (i == 0)) * S.gch + row; };
+    // the first kAhead parts of a thread are on their way while the weights are formed
+    float4 x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int i = grp + k * kGroups;
+        x[k] = i < cnt ? *reinterpret_cast<const float4 *>(S.part + at(i) * D + lane * 4)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float top = -INFINITY;
     for (int i = tid; i < cnt; i += kJoinThreads) {
-        const float2 x = S.ml[((int64_t)(j.z + i) * 2 + (i == 0)) * S.rows + row];
-        w[i] = x;
-        top = fmaxf(top, x.x);
+        const float2 y = S.ml[at(i)];
+        w[i] = y;
+        top = fmaxf(top, y.x);
     }
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if ((tid & 31) == 0) red[tid >> 5] = top;
     __syncthreads();
+#pragma unroll
     for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, red[i]);
     const float ref = top == -INFINITY ? 0.f : top;
-    for (int i = tid; i < cnt; i += kJoinThreads) w[i].x = ex2(w[i].x - ref);
-    __syncthreads();
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int i = grp + k * kGroups;
+        const float f = i < cnt ? ex2(w[i].x - ref) : 0.f;
+        a.x = fmaf(x[k].x, f, a.x), a.y = fmaf(x[k].y, f, a.y);
+        a.z = fmaf(x[k].z, f, a.z), a.w = fmaf(x[k].w, f, a.w);
+    }
+#pragma unroll 4
+    for (int i = grp + kAhead * kGroups; i < cnt; i += kGroups) {
+        const float4 y = *reinterpret_cast<const float4 *>(S.part + at(i) * D + lane * 4);
+        const float f = ex2(w[i].x - ref);
+        a.x = fmaf(y.x, f, a.x), a.y = fmaf(y.y, f, a.y);
+        a.z = fmaf(y.z, f, a.z), a.w = fmaf(y.w, f, a.w);
+    }
+    acc[grp][lane] = a;
     if (tid < 32) {
         float s = 0.f;
-        for (int i = tid; i < cnt; i += 32) s = fmaf(w[i].y, w[i].x, s);
+        for (int i = tid; i < cnt; i += 32) s = fmaf(w[i].y, ex2(w[i].x - ref), s);
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         if (tid == 0) sum_s = s;
     }
-    const int lane = tid % kLanes, grp = tid / kLanes;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = grp; i < cnt; i += kGroups) {
-        const float4 x = *reinterpret_cast<const float4 *>(
-            S.part + (((int64_t)(j.z + i) * 2 + (i == 0)) * S.rows + row) * D + lane * 4);
-        const float f = w[i].x;
-        a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
-        a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
-    }
-    acc[grp][lane] = a;
     __syncthreads();
     if (grp) return;
+#pragma unroll
     for (int i = 1; i < kGroups; ++i) {
-        const float4 x = acc[i][lane];
-        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+        const float4 y = acc[i][lane];
+        a.x += y.x, a.y += y.y, a.z += y.z, a.w += y.w;
     }
-    const float sum = sum_s, inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-    const int64_t at = (int64_t)b * A.Hq + ((it / S.gsplit) * S.hw + h) * A.G + g0 + g;
-    put4<T>(static_cast<T *>(A.out) + at * D + lane * 4,
-            make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
-    if (A.lse && lane == 0) A.lse[at] = (top + log2f(sum)) * kLn2;
+    out(row, a, top, sum_s);
 }
 
 Split make_split(int B, int Hq, int Hkv, int dtype) {
     Split S = {};
     const int G = Hq / Hkv, most = dtype == HGA_BF16 ? 16 : 8;
-    S.hw = Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1;
-    S.kw = kWarps / S.hw;
     S.gsplit = (G + most - 1) / most;
     S.gch = (G + S.gsplit - 1) / S.gsplit;
     S.gsplit = (G + S.gch - 1) / S.gch;
-    S.items = Hkv / S.hw * S.gsplit;
-    S.rows = S.hw * S.gch;
+    S.items = Hkv * S.gsplit;
     S.by_item = (long long)B * S.items <= kMaxCtas;
     return S;
 }
@@ -719,7 +783,7 @@ hga_status run(const PagedArgs &A, const Split &S, cudaStream_t st) {
     k<<<S.n, kThreads, smem, st>>>(A, S);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
     const int entries = S.by_item ? A.B * S.items : S.n;
-    return cuda_status(launch_dependent(k_paged_join<typename Tile::T, D>, dim3(entries, S.rows),
+    return cuda_status(launch_dependent(k_paged_join<typename Tile::T, D>, dim3(entries, S.gch),
                                         dim3(kJoinThreads), 0, st, A, S));
 }
 
@@ -727,13 +791,13 @@ hga_status run(const PagedArgs &A, const Split &S, cudaStream_t st) {
 
 size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int dtype) {
     const Split S = make_split(B, Hq, Hkv, dtype);
-    const size_t rows = (size_t)kMaxCtas * 2 * S.rows;
+    const size_t rows = (size_t)kMaxCtas * 2 * S.gch;
     return up256(rows * D * 4) + up256(rows * sizeof(float2)) + up256(kMaxCtas * sizeof(int4));
 }
 
 hga_status launch_paged_decode(const PagedArgs &A, int dtype, int D, void *ws, cudaStream_t st) {
     Split S = make_split(A.B, A.Hq, A.Hkv, dtype);
-    const size_t rows = (size_t)kMaxCtas * 2 * S.rows;
+    const size_t rows = (size_t)kMaxCtas * 2 * S.gch;
     char *p = static_cast<char *>(ws);
     S.part = reinterpret_cast<float *>(p);
     p += up256(rows * D * 4);

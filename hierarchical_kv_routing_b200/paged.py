@@ -19,13 +19,15 @@ that a call allocates are recorded on that stream.
 from __future__ import annotations
 
 import ctypes
-import dataclasses
-from contextlib import nullcontext
-from typing import Optional
+import functools
+from typing import NamedTuple, Optional
 
 import torch
 
 from . import HGAError, _aligned_span, _check, _dtype_code, _F32, _need, _stream, load
+
+# A small step's call is bound by its host side, so the checks below read each
+# attribute of a tensor once and leave the wording of a refusal to _need.
 
 _I32 = torch.int32
 _P = ctypes.c_void_p
@@ -91,8 +93,7 @@ def declare(lib):
         getattr(lib, f).restype = sz
 
 
-@dataclasses.dataclass(frozen=True)
-class HGARope:
+class HGARope(NamedTuple):
     """A position rotation (hga_rope in include/hga.h).  rotary_dim None: the
     whole head; 0: none.  layout "half" (pairs i, i + R/2) or "interleaved"
     (2i, 2i + 1).  scaling "none", "linear" or "yarn" (factor; for yarn also
@@ -135,9 +136,25 @@ class PagedKVCache:
         self.free_count = torch.full((1,), num_pages, dtype=_I32, **z)
 
 
-def _on(dev):
-    """The call's device made current, where it is not."""
-    return nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+@functools.lru_cache(maxsize=64)
+def _rope(rope: HGARope, D: int) -> _Rope:
+    return rope.c(D)
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda index: torch.cuda.current_stream(index).cuda_stream
+
+
+def _launch(what, fn, dev, stream, *args):
+    """fn(*args, stream) with the call's device current."""
+    st = _raw_stream(dev.index) if stream is None else _stream(stream, dev)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, st)
+    if status:
+        _check(status, what)
 
 
 def _new(shape, dtype, dev, stream):
@@ -151,24 +168,23 @@ def _work(nbytes, dev, workspace, stream):
     """(tensor kept for the call, aligned address, bytes from there)."""
     if workspace is None:
         workspace = _new(nbytes + 256, torch.uint8, dev, stream)
-    else:
-        _need(workspace, "workspace", device=dev)
+        base = (workspace.data_ptr() + 255) & -256
+        return workspace, base, nbytes
+    _need(workspace, "workspace", device=dev)
     return (workspace,) + _aligned_span(workspace.data_ptr(),
                                         workspace.numel() * workspace.element_size(), nbytes)
 
 
-def _ints(t, name, shape, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.device != dev \
-            or t.shape != shape or not t.is_contiguous():
-        _need(t, name, shape, _I32, dev)
-    return t.data_ptr()
-
-
 def _dense(t, name, shape, dtype, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != dev \
-            or t.shape != shape or not t.is_contiguous():
+    """The address of a contiguous tensor of that shape, type and device."""
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape \
+            or t.get_device() != dev.index or not t.is_contiguous():
         _need(t, name, shape, dtype, dev)
     return t.data_ptr()
+
+
+def _ints(t, name, shape, dev):
+    return _dense(t, name, shape, _I32, dev)
 
 
 def _token_stride(t, name, lead, H, D, dtype, dev):
@@ -176,7 +192,7 @@ def _token_stride(t, name, lead, H, D, dtype, dev):
     adjacent, heads D apart, tokens evenly spaced (a view of a fused buffer)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise HGAError(f"{name} must be a CUDA tensor")
-    if t.device != dev:
+    if t.get_device() != dev.index:
         raise HGAError(f"{name} is on {t.device}, the call's tensors are on {dev}")
     if t.dtype is not dtype:
         raise HGAError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -215,25 +231,25 @@ def hga_paged_plan(lens, new_tokens, free_pages, free_count, block_table, page_s
     _count(page_size, "page_size")
     _need(free_pages, "free_pages", dtype=_I32, device=dev)
     P = free_pages.numel()
-    lens_out = _new(B, _I32, dev, stream) if lens_out is None else lens_out
-    free_count_out = _new(1, _I32, dev, stream) if free_count_out is None else free_count_out
-    cu_tokens = _new(B + 1, _I32, dev, stream) if cu_tokens is None else cu_tokens
-    granted = _new(B, _I32, dev, stream) if granted is None else granted
-    slot = _new(n_slots, _I32, dev, stream) if slot is None else slot
-    pos = _new(n_slots, _I32, dev, stream) if pos is None else pos
+    given = (lens_out, free_count_out, cu_tokens, granted, slot, pos)
+    sizes = (B, 1, B + 1, B, n_slots, n_slots)
+    if any(t is None for t in given):
+        # one allocation for what the caller does not bring
+        new = _new(sum(n for t, n in zip(given, sizes) if t is None), _I32, dev, stream)
+        parts = iter(new.split([n for t, n in zip(given, sizes) if t is None]))
+        lens_out, free_count_out, cu_tokens, granted, slot, pos = (
+            next(parts) if t is None else t for t in given)
+    ptr = [t.data_ptr() if g is None else _ints(t, name, (n,), dev) for t, g, n, name in zip(
+        (lens_out, free_count_out, cu_tokens, granted, slot, pos), given, sizes,
+        ("lens_out", "free_count_out", "cu_tokens", "granted", "slot", "pos"))]
     io = _PlanIO(_ints(lens, "lens", (B,), dev), _ints(new_tokens, "new_tokens", (B,), dev),
                  None if release is None else _ints(release, "release", (B,), dev),
                  free_pages.data_ptr(), _ints(free_count, "free_count", (1,), dev),
-                 block_table.data_ptr(), _ints(lens_out, "lens_out", (B,), dev),
-                 _ints(free_count_out, "free_count_out", (1,), dev),
-                 _ints(cu_tokens, "cu_tokens", (B + 1,), dev), _ints(granted, "granted", (B,), dev),
-                 _ints(slot, "slot", (n_slots,), dev), _ints(pos, "pos", (n_slots,), dev))
+                 block_table.data_ptr(), *ptr)
     dims = _PagedDims(B, 0, 0, 0, 0, P, page_size, max_pages)
     ws, base, avail = _work(lib.hga_paged_plan_workspace(B, n_slots), dev, workspace, stream)
-    with _on(dev):
-        st = lib.hga_paged_plan(ctypes.byref(dims), ctypes.byref(io), n_slots, base, avail,
-                                _stream(stream, dev))
-    _check(st, "hga_paged_plan")
+    _launch("hga_paged_plan", lib.hga_paged_plan, dev, stream, ctypes.byref(dims),
+            ctypes.byref(io), n_slots, base, avail)
     return dict(lens=lens_out, free_count=free_count_out, cu_tokens=cu_tokens, granted=granted,
                 slot=slot, pos=pos)
 
@@ -295,7 +311,7 @@ def hga_qk_norm_rope(q, k, v, pos, rope: HGARope, *, q_weight=None, k_weight=Non
         _dense(k_pages, "k_pages", shape, dt, dev)
         if v_pages is not None:
             _dense(v_pages, "v_pages", shape, dt, dev)
-    r = rope.c(D)
+    r = _rope(rope, D)
     if pos is None and r.rotary_dim:
         raise HGAError("pos is needed with a rotation")
     io = _QkIO(q.data_ptr(), k.data_ptr(), None if v is None else v.data_ptr(), qs, ks, vs,
@@ -309,10 +325,8 @@ def hga_qk_norm_rope(q, k, v, pos, rope: HGARope, *, q_weight=None, k_weight=Non
                k_pages.data_ptr() if paged else None,
                v_pages.data_ptr() if v_pages is not None else None, num_slots)
     dims = _TokenDims(*_tokens(lead), Hq, Hkv, D, code)
-    with _on(dev):
-        st = lib.hga_qk_norm_rope(ctypes.byref(dims), ctypes.byref(r), ctypes.byref(io),
-                                  _stream(stream, dev))
-    _check(st, "hga_qk_norm_rope")
+    _launch("hga_qk_norm_rope", lib.hga_qk_norm_rope, dev, stream, ctypes.byref(dims),
+            ctypes.byref(r), ctypes.byref(io))
     return q_out, k_out, v_out
 
 
@@ -343,7 +357,7 @@ def hga_qk_norm_rope_backward(q, k, d_q, d_k, pos, rope: HGARope, *, q_weight=No
     dv = _new(kv, dt, dev, stream) if dv is None and d_v is not None else dv
     dqw = None if q_weight is None else _new(D, torch.float32, dev, stream)
     dkw = None if k_weight is None else _new(D, torch.float32, dev, stream)
-    r = rope.c(D)
+    r = _rope(rope, D)
     if pos is None and r.rotary_dim:
         raise HGAError("pos is needed with a rotation")
     io = _QkGradIO(q.data_ptr(), k.data_ptr(), qs, ks,
@@ -361,10 +375,8 @@ def hga_qk_norm_rope_backward(q, k, d_q, d_k, pos, rope: HGARope, *, q_weight=No
     dims = _TokenDims(*_tokens(lead), Hq, Hkv, D, code)
     ws, base, avail = _work(lib.hga_qk_norm_rope_backward_workspace(ctypes.byref(dims)), dev,
                             workspace, stream)
-    with _on(dev):
-        st = lib.hga_qk_norm_rope_backward(ctypes.byref(dims), ctypes.byref(r), ctypes.byref(io),
-                                           base, avail, _stream(stream, dev))
-    _check(st, "hga_qk_norm_rope_backward")
+    _launch("hga_qk_norm_rope_backward", lib.hga_qk_norm_rope_backward, dev, stream,
+            ctypes.byref(dims), ctypes.byref(r), ctypes.byref(io), base, avail)
     return dq, dk, dv, dqw, dkw
 
 
@@ -397,13 +409,11 @@ def hga_paged_decode(q, k_pages, v_pages, block_table, lens, *, window: int = 0,
     nbytes = lib.hga_paged_decode_workspace(ctypes.byref(dims))
     ws, base, avail = _work(nbytes, dev, workspace, stream)
     pages = (P, page, Hkv, D)
-    with _on(dev):
-        st = lib.hga_paged_decode(
-            ctypes.byref(dims), q.data_ptr(), _dense(k_pages, "k_pages", pages, dt, dev),
+    _launch("hga_paged_decode", lib.hga_paged_decode, dev, stream, ctypes.byref(dims),
+            q.data_ptr(), _dense(k_pages, "k_pages", pages, dt, dev),
             _dense(v_pages, "v_pages", pages, dt, dev),
             _ints(block_table, "block_table", (B, max_pages), dev), _ints(lens, "lens", (B,), dev),
-            _count(window, "window"), _count(sinks, "sinks"), scale, _dense(out, "out", (B, Hq, D), dt, dev),
-            None if lse is None else _dense(lse, "lse", (B, Hq), torch.float32, dev), base, avail,
-            _stream(stream, dev))
-    _check(st, "hga_paged_decode")
+            _count(window, "window"), _count(sinks, "sinks"), scale,
+            _dense(out, "out", (B, Hq, D), dt, dev),
+            None if lse is None else _dense(lse, "lse", (B, Hq), torch.float32, dev), base, avail)
     return (out, lse) if lse is not None else out
