@@ -137,7 +137,6 @@ def load():
         for f in ("hga_build_summaries", "hga_route", "hga_attend", "hga_forward",
                   "hga_attend_backward"):
             getattr(lib, f).restype = ctypes.c_int
-        _declare_paged(lib)
         _lib = lib
         return lib
 
@@ -686,5 +685,5 @@ def hga_forward(mode: int, *args, **kw):
     raise HGAError(f"unknown mode {mode}")
 
 
-from .paged import (HGARope, PagedKVCache, declare as _declare_paged, hga_paged_decode,  # noqa: E402
-                    hga_paged_plan, hga_qk_norm_rope, hga_qk_norm_rope_backward)
+from .paged import (HGARope, PagedKVCache, hga_paged_decode, hga_paged_plan,  # noqa: E402
+                    hga_qk_norm_rope, hga_qk_norm_rope_backward)

@@ -1,16 +1,21 @@
 """Build libhga.so in-tree: every csrc/*.cu compiled for sm_100a with nvcc,
-objects under _build/, linked into hierarchical_kv_routing_b200/libhga.so."""
+objects under _build/, linked into hierarchical_kv_routing_b200/libhga.so; and
+_paged.so, the compiled part of the Python binding (csrc/binding.cpp, host code
+against the installed torch and libhga.so)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libhga.so")
+EXT = os.path.join(PKG, "_paged.so")
+EXT_SRC = os.path.join(CSRC, "binding.cpp")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -20,7 +25,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
 
 
 def _deps_mtime() -> float:
-    files = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    files = glob.glob(os.path.join(CSRC, "*.cu*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     return max(os.path.getmtime(f) for f in files)
 
 
@@ -36,8 +41,35 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_ext(force: bool) -> None:
+    """binding.cpp -> _paged.so (after libhga.so, which it links)."""
+    newest = max(os.path.getmtime(f) for f in [EXT_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= newest:
+        return
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+    inc = [f"-I{p}" for p in [*cpp_extension.include_paths(), cuda, INCLUDE,
+                              sysconfig.get_paths()["include"]]]
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", *inc, EXT_SRC, "-o", tmp,
+           f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-L{PKG}",
+           "-lhga", "-Wl,-rpath,$ORIGIN", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile (incrementally) and link; returns the library path."""
+    _build_lib(force, verbose)
+    _build_ext(force)
+    return LIB
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
     os.makedirs(BUILD, exist_ok=True)
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
         return LIB

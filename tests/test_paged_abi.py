@@ -8,23 +8,59 @@ import pytest
 import torch
 
 import hierarchical_kv_routing_b200 as hga
-from hierarchical_kv_routing_b200 import _build, paged
+from hierarchical_kv_routing_b200 import _build
 from tests import paged_reference as ref
 
 A = 1 << 24
 INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 6
+P, I32, I64, F64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double
+
+
+def struct(name, *fields):
+    """A structure of include/hga.h: (type, "names ...") in order."""
+    return type(name, (ctypes.Structure,), {"_fields_": [(n, t) for t, ns in fields for n in ns.split()]})
+
+
+PagedDims = struct("hga_paged_dims", (I32, "B Hq Hkv D dtype num_pages page_size max_pages"))
+PlanIO = struct("hga_paged_plan_io", (P, "lens new_tokens release free_pages free_count block_table "
+                                         "lens_out free_count_out cu_tokens granted slot pos"))
+Rope = struct("hga_rope", (I32, "layout rotary_dim scaling original_len"),
+              (F64, "theta factor beta_fast beta_slow magnitude"))
+QkIO = struct("hga_qk_io", (P, "q k v"), (I64, "q_stride k_stride v_stride"), (P, "q_weight k_weight"),
+              (F64, "eps"), (P, "pos q_out k_out v_out slot k_pages v_pages"), (I64, "num_slots"))
+GradIO = struct("hga_qk_grad_io", (P, "q k"), (I64, "q_stride k_stride"), (P, "q_weight k_weight"),
+                (F64, "eps"), (P, "pos d_q d_k d_v"), (I32, "grad_dtype"), (P, "dq dk dv"),
+                (I64, "dq_stride dk_stride dv_stride"), (P, "d_q_weight d_k_weight"))
+
+
+def rope(**kw):
+    d = dict(layout=0, rotary_dim=64, scaling=0, original_len=0, theta=1e6, factor=1.0, beta_fast=32.0,
+             beta_slow=1.0, magnitude=0.0)
+    d.update(kw)
+    return Rope(**d)
 
 
 @pytest.fixture(scope="module")
 def lib():
     _build.build()
-    return hga.load()
+    hga.load()
+    lib = ctypes.CDLL(hga.lib_path())             # argument types of this module's own
+    sz = ctypes.c_size_t
+    lib.hga_paged_plan.argtypes = [P, P, I32, P, sz, P]
+    lib.hga_qk_norm_rope.argtypes = [P, P, P, P]
+    lib.hga_qk_norm_rope_backward.argtypes = [P, P, P, P, sz, P]
+    lib.hga_paged_decode.argtypes = [P, P, P, P, P, P, I32, I32, F64, P, P, P, sz, P]
+    lib.hga_paged_plan_workspace.argtypes = [I32, I32]
+    for f in ("plan", "decode"):
+        getattr(lib, f"hga_paged_{f}_workspace").restype = sz
+    lib.hga_qk_norm_rope_backward_workspace.restype = sz
+    return lib
 
 
 def pdims(**kw):
     d = dict(B=4, Hq=8, Hkv=2, D=64, dtype=1, num_pages=100, page_size=16, max_pages=10)
     d.update(kw)
-    return paged._PagedDims(**d)
+    return PagedDims(**d)
 
 
 BAD_PAGES = [(dict(B=0), INVALID), (dict(num_pages=0), INVALID), (dict(page_size=0), INVALID),
@@ -36,9 +72,9 @@ BAD_HEADS = [(dict(Hq=0), INVALID), (dict(Hkv=3), INVALID), (dict(D=96), UNSUPPO
 
 
 def plan_io(**kw):
-    d = {n: A for n, _ in paged._PlanIO._fields_}
+    d = {n: A for n, _ in PlanIO._fields_}
     d.update(kw)
-    return paged._PlanIO(**d)
+    return PlanIO(**d)
 
 
 def call_plan(lib, d, io, n=8, ws=A, nbytes=1 << 20):
@@ -54,7 +90,7 @@ def test_plan_pointers_and_workspace(lib):
     for f in ("lens", "new_tokens", "free_pages", "free_count", "block_table", "lens_out",
               "free_count_out", "cu_tokens", "granted", "slot", "pos"):
         assert call_plan(lib, pdims(), plan_io(**{f: None})) == INVALID, f
-    for f, _ in paged._PlanIO._fields_:
+    for f, _ in PlanIO._fields_:
         assert call_plan(lib, pdims(), plan_io(**{f: A + 2})) == INVALID, f
     assert call_plan(lib, pdims(), plan_io(), n=-1) == INVALID
     assert lib.hga_paged_plan(None, None, 0, None, 0, None) == INVALID
@@ -101,14 +137,14 @@ def test_decode_pointers_values_and_workspace(lib):
 def tdims(**kw):
     d = dict(B=1, T=7, Hq=4, Hkv=2, D=64, dtype=1)
     d.update(kw)
-    return paged._TokenDims(**d)
+    return hga._Dims(**d)
 
 
 def qk_io(**kw):
     d = dict(q=A, k=A, v=A, q_stride=512, k_stride=512, v_stride=512, q_weight=A, k_weight=A, eps=1e-6,
              pos=A, q_out=A, k_out=A, v_out=A)
     d.update(kw)
-    return paged._QkIO(**d)
+    return QkIO(**d)
 
 
 def grad_io(**kw):
@@ -117,16 +153,16 @@ def grad_io(**kw):
     d.update({n: 512 for n in ("q_stride", "k_stride", "dq_stride", "dk_stride", "dv_stride")})
     d.update(eps=1e-6, grad_dtype=1)
     d.update(kw)
-    return paged._QkGradIO(**d)
+    return GradIO(**d)
 
 
-def call_qk(lib, d, io, rope=None):
-    r = rope or hga.HGARope().c(64)
+def call_qk(lib, d, io, r=None):
+    r = r or rope()
     return lib.hga_qk_norm_rope(ctypes.byref(d), ctypes.byref(r), ctypes.byref(io), None)
 
 
-def call_grad(lib, d, io, rope=None, ws=A, nbytes=1 << 24):
-    r = rope or hga.HGARope().c(64)
+def call_grad(lib, d, io, r=None, ws=A, nbytes=1 << 24):
+    r = r or rope()
     return lib.hga_qk_norm_rope_backward(ctypes.byref(d), ctypes.byref(r), ctypes.byref(io), ws, nbytes,
                                          None)
 
@@ -142,25 +178,17 @@ def test_qk_dims(lib, bad, code):
 @pytest.mark.parametrize("bad,code", [
     (dict(rotary_dim=80), INVALID), (dict(rotary_dim=-16), INVALID), (dict(rotary_dim=24), UNSUPPORTED),
     (dict(theta=1.0), INVALID), (dict(theta=float("nan")), INVALID), (dict(theta=float("inf")), INVALID),
-    (dict(scaling="linear", factor=0.5), INVALID), (dict(scaling="linear", factor=float("inf")), INVALID),
-    (dict(scaling="yarn", factor=2.0), INVALID),
-    (dict(scaling="yarn", factor=2.0, original_len=64, beta_slow=0.0), INVALID),
-    (dict(scaling="yarn", factor=2.0, original_len=64, beta_slow=33.0), INVALID),
-    (dict(magnitude=-1.0), INVALID), (dict(magnitude=float("nan")), INVALID)])
+    (dict(scaling=1, factor=0.5), INVALID), (dict(scaling=1, factor=float("inf")), INVALID),
+    (dict(scaling=2, factor=2.0), INVALID),
+    (dict(scaling=2, factor=2.0, original_len=64, beta_slow=0.0), INVALID),
+    (dict(scaling=2, factor=2.0, original_len=64, beta_slow=33.0), INVALID),
+    (dict(magnitude=-1.0), INVALID), (dict(magnitude=float("nan")), INVALID),
+    (dict(layout=2), INVALID), (dict(layout=-1), INVALID), (dict(scaling=3), INVALID)])
 def test_rope_values(lib, bad, code):
-    r = hga.HGARope(**bad).c(64)
-    assert call_qk(lib, tdims(), qk_io(), r) == code
-    assert call_grad(lib, tdims(), grad_io(), r) == code
-    for field, value in (("layout", 2), ("layout", -1), ("scaling", 3)):
-        r = hga.HGARope().c(64)
-        setattr(r, field, value)
-        assert call_qk(lib, tdims(), qk_io(), r) == INVALID
-
-
-def test_rope_names():
-    for kw in (dict(layout="neox"), dict(scaling="ntk")):
-        with pytest.raises(hga.HGAError):
-            hga.HGARope(**kw).c(64)
+    # a good rotation first: the constants kept of it are not used for the bad one
+    assert call_qk(lib, tdims(), qk_io(q=None), rope(rotary_dim=32)) == INVALID
+    assert call_qk(lib, tdims(), qk_io(q=None), rope(**bad)) == code
+    assert call_grad(lib, tdims(), grad_io(d_q=None), rope(**bad)) == code
 
 
 def test_qk_pointers_and_strides(lib):
@@ -210,8 +238,6 @@ def test_binding_refuses_cpu_tensors():
         hga.hga_qk_norm_rope_backward(x, x, x, x, i, hga.HGARope())
     with pytest.raises(hga.HGAError):
         hga.hga_paged_decode(x, x[None], x[None], torch.zeros(2, 3, dtype=torch.int32), i)
-    with pytest.raises(hga.HGAError):
-        paged._count(1 << 31, "window")
 
 
 def test_reference_plan_pins():
