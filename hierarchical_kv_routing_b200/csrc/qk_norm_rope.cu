@@ -1,20 +1,27 @@
 // Per-head RMS norms of queries and keys with the position rotation in the same
 // pass, and its gradient (hga_qk_norm_rope, hga_qk_norm_rope_backward).
 //
-//   r = (mean x^2 + eps)^(-1/2),  y_d = r (x_d A_d + x_d' B_d)
-// where d' is d's partner in its rotation pair, A_d = w_d cos and
-// B_d = -+ w_d' sin (d outside the rotated part: A = w, B = 0): weight and
-// rotation of a dimension are one multiply-add with constants that depend on the
-// token alone, so a row costs a load, a sum of squares and 2 products a value.
+//   r = (mean x^2 + eps)^(-1/2), and for a pair (a, b) of a row
+//   y_a = r (a (w_a cos) - b (w_b sin)),  y_b = r (b (w_b cos) + a (w_a sin))
+// (dimensions outside the rotated part: cos 1, sin 0): weight and rotation are one
+// multiply-add with constants that depend on the token alone.
 //
-// Bound by HBM: every row is read once and written once.  A row is spread over
-// 16 bytes a lane (16 lanes for bf16 heads of 128), a warp takes the rows of one
-// token so that its cos and sin (64-bit fixed-point angles, sincospif) are formed
-// once, kUnroll loads are in flight per lane before the first is used, and the
-// partner of a half-layout pair comes from the lane that holds it by a shuffle.
+// Bound by HBM: every row is read once and written once.  A warp walks tokens and
+// takes a token's rows N at a time (a step: 512 bytes of rows, 16 lanes to a bf16
+// row of 128), so that cos and sin (64-bit fixed-point angles, sincospif) are formed
+// once a token.  The steps ahead, the next tokens' among them, are on their way to
+// a ring of shared memory (cp.async, 16 bytes a lane): kDepth of them per warp keep
+// 100 KB and more in flight per SM whatever the registers hold.  From there a lane
+// reads V / 2 pairs of its row, both members, so that no value crosses lanes and
+// only the sum of squares does; the arithmetic is two-lane fp32.
+// Measured, 32K tokens of 32 + 4 + 4 bf16 heads of 128 (671 MB): 144 us with a
+// 16-byte word per lane loaded to registers and partners exchanged by shuffles
+// (bound by issue and shuffle latency), 121 us with whole pairs per lane and four
+// rows in flight per lane, and with the ring the figures at the kernels below.
 #include <algorithm>
 
 #include "paged_internal.cuh"
+#include "sm100.cuh"
 #include "vec.cuh"
 
 namespace hga {
@@ -23,81 +30,210 @@ __device__ int g_qk_error = 0;
 
 namespace {
 
+using sm100::f2_fma;
+using sm100::f2_mul;
+using sm100::f2_pack;
+using sm100::f2_unpack;
+
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 template <typename T, int D> struct Row {
     static constexpr int V = 16 / (int)sizeof(T);      // values per lane
+    static constexpr int P = V / 2;                    // pairs per lane
     static constexpr int L = D / V;                    // lanes per row
     static constexpr int N = 32 / L;                   // rows per warp and step
 };
 
-// cos and sin (times the magnitude) of the pairs of position p -> cs[R / 2].
-__device__ __forceinline__ void angles(const PairRope &r, int32_t p, float2 *cs) {
-    for (int i = threadIdx.x & 31; i < r.R / 2; i += 32) {
-        // the angle in turns modulo 1 as a wrapping 64-bit product: exact for any p
-        const unsigned long long u = (unsigned long long)(long long)p * r.turn[i];
-        float s, c;
-        sincospif((float)(int)(u >> 32) * 0x1p-31f, &s, &c);
-        cs[i] = make_float2(c * r.magnitude, s * r.magnitude);
+// cos and sin of a token's pairs.  A lane forms those of pairs lane and lane + 32: it
+// keeps their turn rates (an index into the kernel's parameters that differs from
+// lane to lane is read one lane after the other), and the position of its next token
+// is on its way while this one's rows are worked on.  (Both read at each token's
+// start: 44 us instead of 35 for 8K tokens of 32 + 4 + 4 heads of 128.)
+struct Angles {
+    unsigned long long turn[2];
+    __device__ __forceinline__ void begin(const PairRope &r) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) turn[j] = lane + 32 * j < r.R / 2 ? r.turn[lane + 32 * j] : 0;
     }
-    __syncwarp();
-}
+    // the angles of position p, times the magnitude -> cs[R / 2]
+    __device__ __forceinline__ void form(const PairRope &r, int32_t p, float2 *cs) const {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (lane + 32 * j >= r.R / 2) continue;
+            // the angle in turns modulo 1 as a wrapping 64-bit product: exact for any p
+            const unsigned long long u = (unsigned long long)(long long)p * turn[j];
+            float s, c;
+            sincospif((float)(int)(u >> 32) * 0x1p-31f, &s, &c);
+            cs[lane + 32 * j] = make_float2(c * r.magnitude, s * r.magnitude);
+        }
+        __syncwarp();
+    }
+};
 
-// Where a lane's values stand in the rotation: the lane of their partners, the
-// first pair, and whether they are first members of their pairs.
+// The dimensions a lane owns: P at lo and P at hi.  In the half layout these are the
+// first and second members of its pairs (outside the rotated part any two words);
+// in the interleaved layout they are adjacent and alternate.
 struct Place {
-    int partner, pair;
-    float sign;       // of sin in the forward: -1 for first members, +1 for second, 0 outside
+    int lo, hi, pair;     // pair: of its first pair
+    bool turns;           // inside the rotated part
 };
 template <typename T, int D, bool kInter> __device__ __forceinline__ Place place(int R) {
     using W = Row<T, D>;
-    const int lane = threadIdx.x & 31, d0 = (lane % W::L) * W::V;
-    Place p = {lane, 0, 0.f};
-    if (d0 >= R) return p;
-    if (kInter) {
-        p.pair = d0 / 2;
-        p.sign = 1.f;
-    } else if (d0 < R / 2) {
-        p = {lane + R / 2 / W::V, d0, -1.f};
-    } else {
-        p = {lane - R / 2 / W::V, d0 - R / 2, 1.f};
+    const int l = (threadIdx.x & 31) % W::L;
+    Place p = {l * W::V, l * W::V + W::P, l * W::P, l * W::V < R};
+    if (!kInter && p.turns) {
+        p.lo = l * W::P;
+        p.hi = R / 2 + l * W::P;
     }
     return p;
 }
 
-// cos and signed sin of a lane's values (interleaved: even values -sin, odd +sin).
-template <int V, bool kInter>
-__device__ __forceinline__ void trig(const Place &p, const float2 *cs, float (&c)[V], float (&s)[V]) {
+// A lane's part of a row as it lies in memory: 16 bytes (fp32 gradients of bf16
+// rows: 32).
+template <typename T, int P> struct Raw {
+    static constexpr int B = P * (int)sizeof(T) / 4;   // 32-bit words per half: 2 or 4
+    uint32_t w[2 * B];
+};
+template <typename T, int P, bool kInter>
+__device__ __forceinline__ void load_raw(Raw<T, P> &x, const T *row, const Place &p, bool live) {
+    constexpr int B = Raw<T, P>::B;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        c[e] = 1.f;
-        s[e] = 0.f;
-        if (p.sign != 0.f) {
-            const float2 t = cs[p.pair + (kInter ? e / 2 : e)];
-            c[e] = t.x;
-            s[e] = kInter ? (e % 2 ? t.y : -t.y) : p.sign * t.y;
+    for (int i = 0; i < 2 * B; ++i) x.w[i] = 0u;
+    if (!live) return;
+    if constexpr (B == 4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + (h ? p.hi : p.lo)));
+            x.w[4 * h] = v.x, x.w[4 * h + 1] = v.y, x.w[4 * h + 2] = v.z, x.w[4 * h + 3] = v.w;
+        }
+    } else if constexpr (kInter) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + p.lo));
+        x.w[0] = v.x, x.w[1] = v.y, x.w[2] = v.z, x.w[3] = v.w;
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + (h ? p.hi : p.lo)));
+            x.w[2 * h] = v.x, x.w[2 * h + 1] = v.y;
         }
     }
 }
-
-// The partners of a lane's values, given as the 16-byte words that hold them.
-template <typename T, int V, bool kInter, int NW>
-__device__ __forceinline__ void partners(const uint4 (&w)[NW], const float (&x)[V], int src,
-                                         float (&xp)[V]) {
-    if (kInter) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) xp[e] = x[e ^ 1];
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+// the same from shared memory: lo and hi are the addresses of the lane's words
+template <typename T, int P, bool kInter>
+__device__ __forceinline__ void read_raw(Raw<T, P> &x, uint32_t lo, uint32_t hi) {
+    constexpr int B = Raw<T, P>::B;
+    if constexpr (B == 2 && kInter) {
+        const uint4 v = lds128(lo);
+        x.w[0] = v.x, x.w[1] = v.y, x.w[2] = v.z, x.w[3] = v.w;
     } else {
-        uint4 o[NW];
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            o[i].x = __shfl_sync(0xffffffffu, w[i].x, src);
-            o[i].y = __shfl_sync(0xffffffffu, w[i].y, src);
-            o[i].z = __shfl_sync(0xffffffffu, w[i].z, src);
-            o[i].w = __shfl_sync(0xffffffffu, w[i].w, src);
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (B == 4) {
+                const uint4 v = lds128(h ? hi : lo);
+                x.w[4 * h] = v.x, x.w[4 * h + 1] = v.y, x.w[4 * h + 2] = v.z, x.w[4 * h + 3] = v.w;
+            } else {
+                const uint2 v = lds64(h ? hi : lo);
+                x.w[2 * h] = v.x, x.w[2 * h + 1] = v.y;
+            }
         }
-        unpack_words<T, V>(o, xp);
     }
+}
+template <typename T, int P, bool kInter>
+__device__ __forceinline__ void store_raw(T *lo, T *hi, const Raw<T, P> &x) {
+    if constexpr (kInter) {
+        *reinterpret_cast<uint4 *>(lo) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    } else {
+        *reinterpret_cast<uint2 *>(lo) = make_uint2(x.w[0], x.w[1]);
+        *reinterpret_cast<uint2 *>(hi) = make_uint2(x.w[2], x.w[3]);
+    }
+}
+
+// First and second members of the pairs, two values to a 64-bit register.
+template <int P> struct Pairs {
+    uint64_t a[P / 2], b[P / 2];
+};
+template <typename T> __device__ __forceinline__ float value(const uint32_t *w, int i) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+}
+template <typename T, int P, bool kInter>
+__device__ __forceinline__ Pairs<P> unpack(const Raw<T, P> &x) {
+    Pairs<P> y;
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+        if (kInter) {
+            y.a[i] = f2_pack(value<T>(x.w, 4 * i), value<T>(x.w, 4 * i + 2));
+            y.b[i] = f2_pack(value<T>(x.w, 4 * i + 1), value<T>(x.w, 4 * i + 3));
+        } else {
+            y.a[i] = f2_pack(value<T>(x.w, 2 * i), value<T>(x.w, 2 * i + 1));
+            y.b[i] = f2_pack(value<T>(x.w, P + 2 * i), value<T>(x.w, P + 2 * i + 1));
+        }
+    }
+    return y;
+}
+template <typename T, int P, bool kInter>
+__device__ __forceinline__ Raw<T, P> pack(const Pairs<P> &y) {
+    Raw<T, P> x;
+    float v[2 * P];
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+        const float2 a = f2_unpack(y.a[i]), b = f2_unpack(y.b[i]);
+        if (kInter) {
+            v[4 * i] = a.x, v[4 * i + 1] = b.x, v[4 * i + 2] = a.y, v[4 * i + 3] = b.y;
+        } else {
+            v[2 * i] = a.x, v[2 * i + 1] = a.y, v[P + 2 * i] = b.x, v[P + 2 * i + 1] = b.y;
+        }
+    }
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 2 * P; ++i) x.w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            x.w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+    return x;
+}
+
+// cos and sin of a lane's pairs.
+template <int P>
+__device__ __forceinline__ void trig(const Place &p, const float2 *cs, float (&c)[P], float (&s)[P]) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+        const float2 t = p.turns ? cs[p.pair + e] : make_float2(1.f, 0.f);
+        c[e] = t.x;
+        s[e] = t.y;
+    }
+}
+
+template <typename T, int P, bool kInter>
+__device__ __forceinline__ Pairs<P> load_weight(const void *w, const Place &p) {
+    Raw<T, P> x;
+    if (w) {
+        load_raw<T, P, kInter>(x, static_cast<const T *>(w), p, true);
+        return unpack<T, P, kInter>(x);
+    }
+    Pairs<P> y;
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) y.a[i] = y.b[i] = f2_pack(1.f, 1.f);
+    return y;
 }
 
 template <int L> __device__ __forceinline__ float row_sum(float x) {
@@ -105,234 +241,526 @@ template <int L> __device__ __forceinline__ float row_sum(float x) {
     for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
+__device__ __forceinline__ float both(uint64_t x) {
+    const float2 f = f2_unpack(x);
+    return f.x + f.y;
+}
 
-template <typename T, int V> __device__ __forceinline__ void load_weight(const void *w, int d0, float (&x)[V]) {
-    if (w) {
-        load_slice<T, V>(static_cast<const T *>(w) + d0, x);
-    } else {
+// What a call does, by kind of row: 0 queries, 1 keys, 2 values.  The kernels index
+// these with a kind that is the same for the whole warp.
+struct QkWork {
+    int n[3];                  // rows of a token that are wanted
+    int steps[3];              // steps they take
+    int full[3], rest[3];      // steps with all their rows, rows of a ragged last one
+    int H[3];                  // heads: rows of a token in the dense tensors
+    const void *in[3];         // forward: the inputs; gradient: x
+    int64_t in_stride[3];
+    const void *grad[3];       // gradient: dense dy
+    void *out[3];              // forward: dense outputs; gradient: dx
+    int64_t out_stride[3];
+    void *pages[3];
+    const void *weight[3];
+    int split;                 // warps per token
+    unsigned warps;            // tokens * split: below 2^31, as only few tokens are split
+};
+
+// A warp's walk over the rows of its tokens, a step of N rows at a time.  With
+// kSplit, several warps share a token and each takes the steps [s0, s1) of the
+// kinds' steps in a row.  The first `full` steps left of a kind have all their
+// rows; a last one may be ragged.
+template <int N, bool kSplit> struct Walk {
+    unsigned wg, stride, tok;
+    int kind, left, full;      // kind 3: none left
+    int h;                     // first row (0 without kSplit)
+    int s0, s1;
+    __device__ __forceinline__ void begin(const QkWork &K, unsigned first, unsigned stride_) {
+        wg = first, stride = stride_;
+        h = 0;
+        kind = 2;
+        next(K);
+    }
+    // the next kind with steps, of this token or the following ones
+    __device__ __forceinline__ void next(const QkWork &K) {
+        for (;;) {
+            if (kind == 2) {
+                if (wg >= K.warps) {
+                    kind = 3, left = 0;
+                    return;
+                }
+                tok = wg;
+                if (kSplit) {
+                    const unsigned all = (unsigned)(K.steps[0] + K.steps[1] + K.steps[2]);
+                    const unsigned part = wg % (unsigned)K.split;
+                    tok = wg / (unsigned)K.split;
+                    s0 = (int)(all * part / (unsigned)K.split);
+                    s1 = (int)(all * (part + 1) / (unsigned)K.split);
+                }
+                wg += stride;
+                kind = -1;
+            }
+            ++kind;
+            left = K.steps[kind];
+            full = K.full[kind];
+            if (kSplit) {
+                const int at = kind == 0 ? 0 : kind == 1 ? K.steps[0] : K.steps[0] + K.steps[1];
+                const int a = max(s0 - at, 0), b = min(s1 - at, left);
+                h = a * N;
+                left = b - a;
+                full = min(b, full) - a;
+            }
+            if (left > 0) return;
+        }
+    }
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// zeros, and no read, where live is false
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- forward: steps of 2 N rows (1 KB); 128 registers and 64 KB of ring a CTA, two
+// CTAs per SM.
+constexpr int kDepth = 8, kStep = 1024, kCtas = 148 * 2;
+
+// Two rows of a lane (at lo/hi and 512 bytes on in shared memory, N rows on in
+// memory): y = r (x A + x' B), to `to` and, where given, `also`.
+template <typename T, int D, bool kInter, bool kCheck>
+__device__ __forceinline__ void two_rows(uint32_t lo, uint32_t hi, bool norm, float eps,
+                                         const Pairs<Row<T, D>::P> &c, const Pairs<Row<T, D>::P> &s,
+                                         T *to, T *also, int skip, bool live0, bool live1) {
+    using W = Row<T, D>;
+    constexpr int P = W::P;
+    Pairs<P> x[2];
+    float r[2];
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[e] = 1.f;
+    for (int u = 0; u < 2; ++u) {
+        Raw<T, P> raw;
+        read_raw<T, P, kInter>(raw, lo + u * 512, hi + u * 512);
+        x[u] = unpack<T, P, kInter>(raw);
+    }
+    if (norm) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            uint64_t ss = f2_mul(x[u].a[0], x[u].a[0]);
+#pragma unroll
+            for (int e = 1; e < P / 2; ++e) ss = f2_fma(x[u].a[e], x[u].a[e], ss);
+#pragma unroll
+            for (int e = 0; e < P / 2; ++e) ss = f2_fma(x[u].b[e], x[u].b[e], ss);
+            r[u] = both(ss);
+        }
+#pragma unroll
+        for (int o = W::L / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) r[u] += __shfl_xor_sync(0xffffffffu, r[u], o);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) r[u] = rsqrtf(fmaf(r[u], 1.f / D, eps));
+    } else {
+        r[0] = r[1] = 1.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const uint64_t rr = f2_pack(r[u], r[u]);
+        Pairs<P> y;
+#pragma unroll
+        for (int e = 0; e < P / 2; ++e) {
+            y.a[e] = f2_mul(f2_fma(x[u].a[e], c.a[e], f2_mul(x[u].b[e], s.a[e])), rr);
+            y.b[e] = f2_mul(f2_fma(x[u].b[e], c.b[e], f2_mul(x[u].a[e], s.b[e])), rr);
+        }
+        const Raw<T, P> z = pack<T, P, kInter>(y);
+        if (!kCheck || (u ? live1 : live0)) {
+            T *at = to + u * W::N * D;
+            store_raw<T, P, kInter>(at, at + skip, z);
+            if (also) {
+                at = also + u * W::N * D;
+                store_raw<T, P, kInter>(at, at + skip, z);
+            }
+        }
     }
 }
 
-struct QkWork {
-    int nq, nk, nv;    // rows of a token that are wanted
-    int sq, sk, sv;    // steps of W::N rows they take
-    int split;         // warps per token
-};
-
-constexpr int kUnroll = 4;
-
-template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kThreads, 3) k_qk_norm_rope(const QkArgs A, const QkWork K) {
+template <typename T, int D, bool kInter, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 2) k_qk_norm_rope(const QkArgs A, const QkWork K) {
     using W = Row<T, D>;
-    constexpr int V = W::V;
+    constexpr int P = W::P, N2 = 2 * W::N, E = (int)sizeof(T);
     __shared__ float2 cs_all[kWarps][kMaxHalf];
+    extern __shared__ __align__(16) char ring_all[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / W::L;
-    const int d0 = (lane % W::L) * V;
-    const int64_t wg = (int64_t)blockIdx.x * kWarps + warp;
-    const int64_t tok = wg / K.split;
-    if (tok >= A.tokens) return;
-    const int steps = K.sq + K.sk + K.sv, part = (int)(wg % K.split);
-    const int s0 = (int)((int64_t)steps * part / K.split);
-    const int s1 = (int)((int64_t)steps * (part + 1) / K.split);
-    int64_t slot = -1;
-    if (A.io.slot && s1 > K.sq) {
-        slot = A.io.slot[tok];
-        if (slot < -1 || slot >= A.io.num_slots) {
-            if (lane == 0) atomicExch(&g_qk_error, (int)HGA_ERR_BOUNDS);
-            slot = -1;
+    const int d0 = (lane % W::L) * W::V;
+    const unsigned first = blockIdx.x * (unsigned)kWarps + warp, stride = gridDim.x * kWarps;
+    const uint32_t ring = sm100::smem_addr(ring_all) + warp * kDepth * kStep, mine = ring + lane * 16;
+    float2 *cs = cs_all[warp];
+    const Place pl = place<T, D, kInter>(A.rope.R);
+    const uint32_t lo = ring + (sub * D + pl.lo) * E, hi = ring + (sub * D + pl.hi) * E;
+    const float eps = (float)A.io.eps;
+
+    // ---- the steps ahead
+    Walk<N2, kSplit> p = {};
+    const T *src = nullptr;
+    auto find = [&]() {
+        if (p.kind == 3) return;
+        src = static_cast<const T *>(K.in[p.kind]) + p.tok * K.in_stride[p.kind] + (p.h + sub) * D + d0;
+    };
+    p.begin(K, first, stride);
+    find();
+    auto issue = [&](uint32_t at) {               // at: offset of a ring slot
+        if (p.left > 0) {
+            if (p.full > 0) {
+                cp16(mine + at, src);
+                cp16(mine + at + 512, src + W::N * D);
+                --p.full;
+            } else {
+                // rows beyond the last are zeros; the address given for them is row 0's
+                const int rest = K.rest[p.kind];
+                const T *row0 = src - sub * D;
+                cp16(mine + at, sub < rest ? src : row0, sub < rest);
+                cp16(mine + at + 512, sub + W::N < rest ? src + W::N * D : row0, sub + W::N < rest);
+            }
+            src += N2 * D;
+            if (--p.left == 0) {
+                p.next(K);
+                find();
+            }
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) issue(i * kStep);
+
+    // ---- the rows at hand
+    Walk<N2, kSplit> c = {};
+    c.begin(K, first, stride);
+    Angles ang;
+    ang.begin(A.rope);
+    int32_t next_pos = 0, next_row = -1;          // of the token that comes next
+    auto ahead = [&](unsigned wg) {
+        if (wg >= K.warps) return;
+        const unsigned t = kSplit ? wg / (unsigned)K.split : wg;
+        if (A.rope.R) next_pos = A.io.pos[t];
+        if (A.io.slot) next_row = A.io.slot[t];
+    };
+    ahead(first);
+    unsigned tok = ~0u;
+    int page_row = -1;
+    uint32_t at = 0, to_fill = (kDepth - 1) * kStep;     // ring offsets
+    auto step = [&]() {                           // makes the next step's rows readable
+        __syncwarp();                             // the slot filled now has been read
+        issue(to_fill);
+        to_fill = to_fill == (kDepth - 1) * kStep ? 0 : to_fill + kStep;
+        cp_wait<kDepth - 1>();
+        __syncwarp();
+    };
+    auto done = [&]() { at = at == (kDepth - 1) * kStep ? 0 : at + kStep; };
+    for (; c.kind < 3; c.next(K)) {
+        if (c.tok != tok) {                       // a new token: its angles and its slot
+            tok = c.tok;
+            const int32_t pos = next_pos;
+            page_row = next_row;
+            ahead(c.wg);
+            if (A.rope.R && c.kind < 2) ang.form(A.rope, pos, cs);
+            if (page_row < -1 || page_row >= A.io.num_slots) {
+                if (A.io.slot && lane == 0) atomicExch(&g_qk_error, (int)HGA_ERR_BOUNDS);
+                page_row = -1;
+            }
+        }
+        // where the rows go: `to`, and `also` where both are wanted
+        const int rest = K.rest[c.kind], off = (c.h + sub) * D + (c.kind == 2 ? d0 : pl.lo);
+        void *pages = page_row < 0 ? nullptr : K.pages[c.kind];
+        T *to = static_cast<T *>(K.out[c.kind]);
+        T *also = static_cast<T *>(pages);
+        if (to) to += tok * (int64_t)(K.H[c.kind] * D) + off;
+        if (also) also += page_row * (int64_t)(K.H[c.kind] * D) + off;
+        if (!to) to = also, also = nullptr;
+        if (!to) {                                // nowhere: read and dropped
+            for (int n = c.left; n > 0; --n) {
+                step();
+                done();
+            }
+            continue;
+        }
+        const bool live0 = sub < rest, live1 = sub + W::N < rest;   // of a ragged last step
+        if (c.kind == 2) {                        // values: copied
+            for (int n = c.left; n > 0; --n, --c.full) {
+                step();
+                const uint4 x = lds128(mine + at), y = lds128(mine + at + 512);
+                done();
+                if (c.full > 0 || live0) {
+                    *reinterpret_cast<uint4 *>(to) = x;
+                    if (also) *reinterpret_cast<uint4 *>(also) = x;
+                }
+                if (c.full > 0 || live1) {
+                    *reinterpret_cast<uint4 *>(to + W::N * D) = y;
+                    if (also) *reinterpret_cast<uint4 *>(also + W::N * D) = y;
+                }
+                to += N2 * D;
+                if (also) also += N2 * D;
+            }
+            continue;
+        }
+        const void *weight = K.weight[c.kind];
+        const bool norm = weight != nullptr;
+        Pairs<P> ct, st;                          // w_a cos, w_b cos; -w_b sin, w_a sin
+        {
+            float cf[P], tf[P];
+            trig<P>(pl, cs, cf, tf);
+            const Pairs<P> w = load_weight<T, P, kInter>(weight, pl);
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) {
+                const uint64_t cc = f2_pack(cf[2 * i], cf[2 * i + 1]);
+                ct.a[i] = f2_mul(w.a[i], cc);
+                ct.b[i] = f2_mul(w.b[i], cc);
+                st.a[i] = f2_mul(w.b[i], f2_pack(-tf[2 * i], -tf[2 * i + 1]));
+                st.b[i] = f2_mul(w.a[i], f2_pack(tf[2 * i], tf[2 * i + 1]));
+            }
+        }
+        const int skip = pl.hi - pl.lo, ragged = c.left - c.full;
+        for (int n = c.full; n > 0; --n) {
+            step();
+            two_rows<T, D, kInter, false>(lo + at, hi + at, norm, eps, ct, st, to, also, skip, true, true);
+            done();
+            to += N2 * D;
+            if (also) also += N2 * D;
+        }
+        if (ragged) {
+            step();
+            two_rows<T, D, kInter, true>(lo + at, hi + at, norm, eps, ct, st, to, also, skip, live0, live1);
+            done();
         }
     }
-    float2 *cs = cs_all[warp];
-    if (A.rope.R && s0 < K.sq + K.sk) angles(A.rope, A.io.pos[tok], cs);
-    const Place pl = place<T, D, kInter>(A.rope.R);
-
-    // rows of one kind: steps [a, b) of its own numbering
-    auto rows = [&](int a, int b, int count, const void *src, int64_t stride, const void *weight,
-                    void *dense, int H, void *pages, bool turn) {
-        if (a >= b) return;
-        float ca[V], cb[V];
-        if (turn) {
-            float w[V], wp[V];
-            trig<V, kInter>(pl, cs, ca, cb);
-            load_weight<T, V>(weight, d0, w);
-            if (kInter) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) wp[e] = w[e ^ 1];
-            } else {
-                load_weight<T, V>(weight, (pl.partner % W::L) * V, wp);
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                ca[e] *= w[e];
-                cb[e] *= wp[e];
-            }
-        }
-        const T *in = static_cast<const T *>(src) + tok * stride + d0;
-        T *out = dense ? static_cast<T *>(dense) + tok * H * D + d0 : nullptr;
-        T *pg = pages && slot >= 0 ? static_cast<T *>(pages) + slot * H * D + d0 : nullptr;
-        for (int i = a; i < b; i += kUnroll) {
-            uint4 x4[kUnroll][1];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int h = (i + u) * W::N + sub;
-                if (i + u < b && h < count) x4[u][0] = __ldg(reinterpret_cast<const uint4 *>(in + h * D));
-                else x4[u][0] = make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                if (i + u >= b) break;                 // the same for the whole warp
-                const int h = (i + u) * W::N + sub;
-                if (turn) {
-                    float x[V], xp[V], y[V], r = 1.f;
-                    unpack_words<T, V>(x4[u], x);
-                    partners<T, V, kInter>(x4[u], x, pl.partner, xp);
-                    if (weight) {
-                        float ss = 0.f;
-#pragma unroll
-                        for (int e = 0; e < V; ++e) ss = fmaf(x[e], x[e], ss);
-                        r = rsqrtf(row_sum<W::L>(ss) * (1.f / D) + (float)A.io.eps);
-                    }
-#pragma unroll
-                    for (int e = 0; e < V; ++e) y[e] = r * fmaf(x[e], ca[e], xp[e] * cb[e]);
-                    alignas(16) T packed[V];
-                    store_slice<T, V>(packed, y);
-                    x4[u][0] = *reinterpret_cast<const uint4 *>(packed);
-                }
-                if (h < count) {
-                    if (out) *reinterpret_cast<uint4 *>(out + h * D) = x4[u][0];
-                    if (pg) *reinterpret_cast<uint4 *>(pg + h * D) = x4[u][0];
-                }
-            }
-        }
-    };
-    rows(s0, min(s1, K.sq), K.nq, A.io.q, A.io.q_stride, A.io.q_weight, A.io.q_out, A.Hq, nullptr, true);
-    rows(max(s0 - K.sq, 0), min(s1 - K.sq, K.sk), K.nk, A.io.k, A.io.k_stride, A.io.k_weight,
-         A.io.k_out, A.Hkv, A.io.k_pages, true);
-    rows(max(s0 - K.sq - K.sk, 0), s1 - K.sq - K.sk, K.nv, A.io.v, A.io.v_stride, nullptr, A.io.v_out,
-         A.Hkv, A.io.v_pages, false);
+    cp_wait<0>();
 }
 
 // ---- gradient.  With g = R^T dy, u = g w:
 //   dw_d += g_d x_d r,   dx = r u - x r^3 mean(u x)
 // A warp walks tokens in a fixed order and keeps the sums of its lanes' weight
 // gradients in registers; a CTA adds its warps', k_qk_weight_grad the CTAs'.
-constexpr int kGradUnroll = 2, kGradCtas = 148 * 2;
+// Steps of N rows; 128 registers and at most 48 KB of ring a CTA, two CTAs per SM.
+constexpr int kGradDepth = 4, kGradCtas = 148 * 2;
 
-template <typename T, typename G, int D, bool kInter>
+template <typename T, typename G> constexpr int grad_step() {    // bytes of a step: x and dy
+    return 512 + 512 * (int)(sizeof(G) / sizeof(T));
+}
+
+template <typename T, typename G, int D, bool kInter, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, const QkWork K) {
     using W = Row<T, D>;
-    constexpr int V = W::V, GW = V * (int)sizeof(G) / 16;
+    constexpr int P = W::P, V = W::V, GW = (int)(sizeof(G) / sizeof(T)), S = grad_step<T, G>();
+    constexpr int E = (int)sizeof(T), EG = (int)sizeof(G);
+    extern __shared__ __align__(16) char ring_all[];
     __shared__ float2 cs_all[kWarps][kMaxHalf];
-    __shared__ float red[kWarps][2][D];
     asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / W::L;
     const int d0 = (lane % W::L) * V;
-    const Place pl = place<T, D, kInter>(A.rope.R);
-    const int steps = K.sq + K.sk + K.sv;
+    const unsigned first = blockIdx.x * (unsigned)kWarps + warp, stride = gridDim.x * kWarps;
+    const uint32_t ring = sm100::smem_addr(ring_all) + warp * kGradDepth * S;
     float2 *cs = cs_all[warp];
-    float wq[V], wk[V], sumq[V], sumk[V];
-    load_weight<T, V>(A.io.q_weight, d0, wq);
-    load_weight<T, V>(A.io.k_weight, d0, wk);
-#pragma unroll
-    for (int e = 0; e < V; ++e) sumq[e] = sumk[e] = 0.f;
+    const Place pl = place<T, D, kInter>(A.rope.R);
+    const float eps = (float)A.io.eps;
+    // a lane's words of a step's slot: x at 0, dy at 512
+    const uint32_t xlo = ring + (sub * D + pl.lo) * E, xhi = ring + (sub * D + pl.hi) * E;
+    const uint32_t glo = ring + 512 + (sub * D + pl.lo) * EG, ghi = ring + 512 + (sub * D + pl.hi) * EG;
 
-    for (int64_t wg = (int64_t)blockIdx.x * kWarps + warp; wg < A.tokens * K.split;
-         wg += (int64_t)gridDim.x * kWarps) {
-        const int64_t tok = wg / K.split;
-        const int part = (int)(wg % K.split);
-        const int s0 = (int)((int64_t)steps * part / K.split);
-        const int s1 = (int)((int64_t)steps * (part + 1) / K.split);
-        __syncwarp();
-        if (A.rope.R && s0 < K.sq + K.sk) angles(A.rope, A.io.pos[tok], cs);
-        float c[V], s[V];
-        trig<V, kInter>(pl, cs, c, s);      // R^T: cos and minus the forward's signed sin
-
-        auto rows = [&](int a, int b, int count, const void *src, int64_t stride, const float (&w)[V],
-                        bool norm, const void *dsrc, void *dst, int64_t dstride, int H,
-                        float (&sum)[V]) {
-            const T *in = static_cast<const T *>(src) + tok * stride + d0;
-            const G *gin = static_cast<const G *>(dsrc) + tok * H * D + d0;
-            T *out = static_cast<T *>(dst) + tok * dstride + d0;
-            for (int i = a; i < b; i += kGradUnroll) {
-                uint4 x4[kGradUnroll][1], g4[kGradUnroll][GW];
+    // ---- the steps ahead
+    Walk<W::N, kSplit> p = {};
+    const T *src = nullptr;
+    const char *gsrc = nullptr;
+    bool has_x = false;
+    auto find = [&]() {
+        if (p.kind == 3) return;
+        has_x = K.weight[p.kind] != nullptr;
+        if (has_x)
+            src = static_cast<const T *>(K.in[p.kind]) + p.tok * K.in_stride[p.kind] + (p.h + sub) * D + d0;
+        gsrc = static_cast<const char *>(K.grad[p.kind]) +
+               (p.tok * (int64_t)(K.H[p.kind] * D) + (p.h + sub) * D) * EG + (lane % W::L) * 16;
+    };
+    const uint32_t xto = ring + lane * 16, gto = ring + 512 + sub * D * EG + (lane % W::L) * 16;
+    p.begin(K, first, stride);
+    find();
+    auto issue = [&](uint32_t at) {
+        if (p.left > 0) {
+            if (p.full > 0) {
+                if (has_x) cp16(xto + at, src);
 #pragma unroll
-                for (int u = 0; u < kGradUnroll; ++u) {
-                    const int h = (i + u) * W::N + sub;
-                    const bool live = i + u < b && h < count;
-                    x4[u][0] = make_uint4(0u, 0u, 0u, 0u);
-                    if (live && norm) x4[u][0] = __ldg(reinterpret_cast<const uint4 *>(in + h * D));
+                for (int j = 0; j < GW; ++j)     // a row's 16-byte words, L at a time
+                    cp16(gto + at + j * W::L * 16, gsrc + j * W::L * 16);
+                --p.full;
+            } else {
+                const int rest = K.rest[p.kind];
+                const bool live = sub < rest;     // for the others: zeros, and row 0's address
+                if (has_x) cp16(xto + at, live ? src : src - sub * D, live);
 #pragma unroll
-                    for (int j = 0; j < GW; ++j)
-                        g4[u][j] = live ? __ldg(reinterpret_cast<const uint4 *>(gin + h * D) + j)
-                                        : make_uint4(0u, 0u, 0u, 0u);
-                }
-#pragma unroll
-                for (int u = 0; u < kGradUnroll; ++u) {
-                    if (i + u >= b) break;
-                    const int h = (i + u) * W::N + sub;
-                    float x[V], g[V], gp[V];
-                    unpack_words<T, V>(x4[u], x);
-                    unpack_words<G, V>(g4[u], g);
-                    partners<G, V, kInter>(g4[u], g, pl.partner, gp);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) g[e] = fmaf(g[e], c[e], -gp[e] * s[e]);
-                    if (norm) {
-                        float ss = 0.f, ux = 0.f;
-#pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            ss = fmaf(x[e], x[e], ss);
-                            ux = fmaf(g[e] * w[e], x[e], ux);
-                        }
-                        ss = row_sum<W::L>(ss);
-                        ux = row_sum<W::L>(ux);
-                        const float r = rsqrtf(ss * (1.f / D) + (float)A.io.eps);
-                        // a row beyond the count is all zeros: with eps 0 its r is infinite
-                        const float rr = h < count ? r : 0.f;
-                        const float f = rr * rr * rr * ux * (1.f / D);
-#pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            sum[e] = fmaf(g[e] * x[e], rr, sum[e]);
-                            g[e] = fmaf(rr, g[e] * w[e], -x[e] * f);
-                        }
-                    }
-                    if (h < count) store_slice<T, V>(out + h * D, g);
-                }
+                for (int j = 0; j < GW; ++j)
+                    cp16(gto + at + j * W::L * 16,
+                         (live ? gsrc : gsrc - sub * D * EG) + j * W::L * 16, live);
             }
-        };
-        rows(s0, min(s1, K.sq), K.nq, A.io.q, A.io.q_stride, wq, A.io.q_weight != nullptr, A.io.d_q,
-             A.io.dq, A.io.dq_stride, A.Hq, sumq);
-        rows(max(s0 - K.sq, 0), min(s1 - K.sq, K.sk), K.nk, A.io.k, A.io.k_stride, wk,
-             A.io.k_weight != nullptr, A.io.d_k, A.io.dk, A.io.dk_stride, A.Hkv, sumk);
-        // values: rounded to the inputs' type
-        const G *gin = static_cast<const G *>(A.io.d_v) + tok * A.Hkv * D + d0;
-        T *out = static_cast<T *>(A.io.dv) + tok * A.io.dv_stride + d0;
-        for (int i = max(s0 - K.sq - K.sk, 0); i < s1 - K.sq - K.sk; ++i) {
-            const int h = i * W::N + sub;
-            if (h >= K.nv) continue;
-            float g[V];
-            load_slice<G, V>(gin + h * D, g);
-            store_slice<T, V>(out + h * D, g);
+            src += W::N * D;
+            gsrc += W::N * D * EG;
+            if (--p.left == 0) {
+                p.next(K);
+                find();
+            }
+        }
+        cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kGradDepth - 1; ++i) issue(i * S);
+
+    const Pairs<P> wq = load_weight<T, P, kInter>(A.io.q_weight, pl),
+                   wk = load_weight<T, P, kInter>(A.io.k_weight, pl);
+    Pairs<P> sumq, sumk;
+#pragma unroll
+    for (int e = 0; e < P / 2; ++e) sumq.a[e] = sumq.b[e] = sumk.a[e] = sumk.b[e] = f2_pack(0.f, 0.f);
+
+    // ---- the rows at hand
+    Walk<W::N, kSplit> c = {};
+    c.begin(K, first, stride);
+    Angles ang;
+    ang.begin(A.rope);
+    int32_t next_pos = 0;                         // of the token that comes next
+    auto ahead = [&](unsigned wg) {
+        if (wg < K.warps && A.rope.R) next_pos = A.io.pos[kSplit ? wg / (unsigned)K.split : wg];
+    };
+    ahead(first);
+    unsigned tok = ~0u;
+    uint32_t at = 0, to_fill = (kGradDepth - 1) * S;     // ring offsets
+    auto step = [&]() {                           // makes the next step's rows readable
+        __syncwarp();                             // the slot filled now has been read
+        issue(to_fill);
+        to_fill = to_fill == (kGradDepth - 1) * S ? 0 : to_fill + S;
+        cp_wait<kGradDepth - 1>();
+        __syncwarp();
+    };
+    auto done = [&]() { at = at == (kGradDepth - 1) * S ? 0 : at + S; };
+    uint64_t cc[P / 2], tt[P / 2], tn[P / 2];
+    // one row of a lane; live: it exists (a ragged last step's others are zeros)
+    auto row = [&](const Pairs<P> &w, bool norm, T *out, bool live, Pairs<P> &sum) {
+        step();
+        Raw<G, P> graw;
+        read_raw<G, P, kInter>(graw, glo + at, ghi + at);
+        const Pairs<P> d = unpack<G, P, kInter>(graw);
+        Pairs<P> g;
+#pragma unroll
+        for (int e = 0; e < P / 2; ++e) {
+            g.a[e] = f2_fma(d.a[e], cc[e], f2_mul(d.b[e], tt[e]));
+            g.b[e] = f2_fma(d.b[e], cc[e], f2_mul(d.a[e], tn[e]));
+        }
+        if (norm) {
+            Raw<T, P> raw;
+            read_raw<T, P, kInter>(raw, xlo + at, xhi + at);
+            const Pairs<P> x = unpack<T, P, kInter>(raw);
+            Pairs<P> u;
+            uint64_t s2 = f2_mul(x.a[0], x.a[0]), s1x;
+#pragma unroll
+            for (int e = 0; e < P / 2; ++e) {
+                u.a[e] = f2_mul(g.a[e], w.a[e]);
+                u.b[e] = f2_mul(g.b[e], w.b[e]);
+                if (e) s2 = f2_fma(x.a[e], x.a[e], s2);
+                s2 = f2_fma(x.b[e], x.b[e], s2);
+                s1x = e ? f2_fma(u.a[e], x.a[e], s1x) : f2_mul(u.a[e], x.a[e]);
+                s1x = f2_fma(u.b[e], x.b[e], s1x);
+            }
+            float ss = both(s2), ux = both(s1x);
+#pragma unroll
+            for (int o = W::L / 2; o > 0; o >>= 1) {
+                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                ux += __shfl_xor_sync(0xffffffffu, ux, o);
+            }
+            // a row that does not exist is all zeros: with eps 0 its r is infinite
+            const float r = live ? rsqrtf(fmaf(ss, 1.f / D, eps)) : 0.f;
+            const float f = -r * r * r * ux * (1.f / D);
+            const uint64_t rr = f2_pack(r, r), ff = f2_pack(f, f);
+#pragma unroll
+            for (int e = 0; e < P / 2; ++e) {
+                sum.a[e] = f2_fma(f2_mul(g.a[e], x.a[e]), rr, sum.a[e]);
+                sum.b[e] = f2_fma(f2_mul(g.b[e], x.b[e]), rr, sum.b[e]);
+                g.a[e] = f2_fma(x.a[e], ff, f2_mul(u.a[e], rr));
+                g.b[e] = f2_fma(x.b[e], ff, f2_mul(u.b[e], rr));
+            }
+        }
+        done();
+        if (live) store_raw<T, P, kInter>(out, out + (pl.hi - pl.lo), pack<T, P, kInter>(g));
+    };
+    auto rows = [&](const Pairs<P> &w, bool norm, T *out, int rest, Pairs<P> &sum) {
+        const int ragged = c.left - c.full;
+        for (int n = c.full; n > 0; --n) {
+            row(w, norm, out, true, sum);
+            out += W::N * D;
+        }
+        if (ragged) row(w, norm, out, sub < rest, sum);
+    };
+    for (; c.kind < 3; c.next(K)) {
+        if (c.tok != tok) {
+            tok = c.tok;
+            const int32_t pos = next_pos;
+            ahead(c.wg);
+            if (A.rope.R && c.kind < 2) ang.form(A.rope, pos, cs);
+            float cf[P], tf[P];
+            trig<P>(pl, cs, cf, tf);
+#pragma unroll
+            for (int e = 0; e < P / 2; ++e) {
+                cc[e] = f2_pack(cf[2 * e], cf[2 * e + 1]);
+                tt[e] = f2_pack(tf[2 * e], tf[2 * e + 1]);
+                tn[e] = f2_pack(-tf[2 * e], -tf[2 * e + 1]);
+            }
+        }
+        T *out = static_cast<T *>(K.out[c.kind]) + tok * K.out_stride[c.kind] + (c.h + sub) * D;
+        const int rest = K.rest[c.kind];
+        if (c.kind == 0) {
+            rows(wq, K.weight[0] != nullptr, out + pl.lo, rest, sumq);
+        } else if (c.kind == 1) {
+            rows(wk, K.weight[1] != nullptr, out + pl.lo, rest, sumk);
+        } else {                                  // values: rounded to the inputs' type
+            out += d0;
+            for (int n = c.left; n > 0; --n, --c.full) {
+                step();
+                uint4 raw[GW];
+#pragma unroll
+                for (int j = 0; j < GW; ++j) raw[j] = lds128(ring + at + 512 + (sub * D + d0) * EG + j * 16);
+                done();
+                float g[V];
+                unpack_words<G, V>(raw, g);
+                if (c.full > 0 || sub < rest) store_slice<T, V>(out, g);
+                out += W::N * D;
+            }
         }
     }
+    cp_wait<0>();
     if (!A.part) return;
+    // a lane's sums in the order of its dimensions, in the ring's place
+    float *red = reinterpret_cast<float *>(ring_all + warp * kGradDepth * S);
+    __syncwarp();
+    auto put = [&](const Pairs<P> &sum, float *dst) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
+        for (int e = 0; e < P; ++e) {
+            float a = e % 2 ? f2_unpack(sum.a[e / 2]).y : f2_unpack(sum.a[e / 2]).x;
+            float b = e % 2 ? f2_unpack(sum.b[e / 2]).y : f2_unpack(sum.b[e / 2]).x;
 #pragma unroll
-        for (int o = W::L; o < 32; o <<= 1) {
-            sumq[e] += __shfl_xor_sync(0xffffffffu, sumq[e], o);
-            sumk[e] += __shfl_xor_sync(0xffffffffu, sumk[e], o);
+            for (int o = W::L; o < 32; o <<= 1) {
+                a += __shfl_xor_sync(0xffffffffu, a, o);
+                b += __shfl_xor_sync(0xffffffffu, b, o);
+            }
+            if (sub == 0) {
+                dst[kInter ? pl.lo + 2 * e : pl.lo + e] = a;
+                dst[kInter ? pl.lo + 2 * e + 1 : pl.hi + e] = b;
+            }
         }
-        if (sub == 0) {
-            red[warp][0][d0 + e] = sumq[e];
-            red[warp][1][d0 + e] = sumk[e];
-        }
-    }
+    };
+    static_assert(kGradDepth * S >= 2 * D * 4, "a warp's sums fit its ring");
+    put(sumq, red);
+    put(sumk, red + D);
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
         float x = 0.f;
-        for (int w = 0; w < kWarps; ++w) x += red[w][i / D][i % D];
+        for (int w = 0; w < kWarps; ++w)
+            x += reinterpret_cast<const float *>(ring_all + w * kGradDepth * S)[i];
         A.part[(int64_t)blockIdx.x * 2 * D + i] = x;
     }
 }
@@ -357,46 +785,64 @@ __global__ void __launch_bounds__(1024) k_qk_weight_grad(const float *part, int 
     if (dst) dst[c % D] = s;
 }
 
-template <typename T, int D> QkWork make_work(int64_t tokens, int nq, int nk, int nv) {
-    constexpr int N = Row<T, D>::N;
-    QkWork K;
-    K.nq = nq, K.nk = nk, K.nv = nv;
-    K.sq = (nq + N - 1) / N, K.sk = (nk + N - 1) / N, K.sv = (nv + N - 1) / N;
+// N: rows of a step
+void set_work(QkWork &K, int N, int64_t tokens) {
+    int steps = 0;
+    for (int i = 0; i < 3; ++i) {
+        K.full[i] = K.n[i] / N;
+        K.rest[i] = K.n[i] % N;
+        K.steps[i] = K.full[i] + (K.rest[i] > 0);
+        steps += K.steps[i];
+    }
     // a warp per token where that fills the card; fewer tokens are spread over more
     // warps (each forms the angles again), down to one step a warp
     const int64_t want = 148 * 16;
-    const int steps = std::max(1, K.sq + K.sk + K.sv);
-    K.split = tokens == 0 ? 1 : (int)std::min<int64_t>(steps, std::max<int64_t>(1, (want + tokens - 1) / tokens));
-    return K;
+    K.split = tokens == 0 ? 1 : (int)std::min<int64_t>(std::max(steps, 1), std::max<int64_t>(1, (want + tokens - 1) / tokens));
+    K.warps = (unsigned)(tokens * K.split);
 }
 
 template <typename T, int D> hga_status forward(const QkArgs &A, cudaStream_t st) {
-    const QkWork K = make_work<T, D>(A.tokens, A.io.q_out ? A.Hq : 0,
-                                     A.io.k_out || A.io.k_pages ? A.Hkv : 0,
-                                     A.io.v_out || A.io.v_pages ? A.Hkv : 0);
-    if (K.sq + K.sk + K.sv == 0) return HGA_OK;
-    const unsigned grid = (unsigned)((A.tokens * K.split + kWarps - 1) / kWarps);
-    if (A.rope.interleaved) k_qk_norm_rope<T, D, true><<<grid, kThreads, 0, st>>>(A, K);
-    else k_qk_norm_rope<T, D, false><<<grid, kThreads, 0, st>>>(A, K);
+    const hga_qk_io &io = A.io;
+    QkWork K = {{io.q_out ? A.Hq : 0, io.k_out || io.k_pages ? A.Hkv : 0, io.v_out || io.v_pages ? A.Hkv : 0},
+                {}, {}, {}, {A.Hq, A.Hkv, A.Hkv}, {io.q, io.k, io.v},
+                {io.q_stride, io.k_stride, io.v_stride}, {}, {io.q_out, io.k_out, io.v_out}, {},
+                {nullptr, io.k_pages, io.v_pages}, {io.q_weight, io.k_weight, nullptr}, 1, 0u};
+    set_work(K, 2 * Row<T, D>::N, A.tokens);
+    if (K.steps[0] + K.steps[1] + K.steps[2] == 0) return HGA_OK;
+    const unsigned grid = std::min<unsigned>(kCtas, (K.warps + kWarps - 1) / kWarps);
+    auto *k = A.rope.interleaved ? K.split > 1 ? k_qk_norm_rope<T, D, true, true> : k_qk_norm_rope<T, D, true, false>
+              : K.split > 1      ? k_qk_norm_rope<T, D, false, true>
+                                 : k_qk_norm_rope<T, D, false, false>;
+    const size_t smem = (size_t)kWarps * kDepth * kStep;
+    const cudaError_t e = ensure_smem((const void *)k, smem);
+    if (e != cudaSuccess) return cuda_status(e);
+    k<<<grid, kThreads, smem, st>>>(A, K);
     return cuda_status(cudaGetLastError());
 }
 
 template <typename T, typename G, int D> hga_status backward(const QkGradArgs &A0, cudaStream_t st) {
     QkGradArgs A = A0;
-    const bool weights = A.io.d_q_weight || A.io.d_k_weight;
+    const hga_qk_grad_io &io = A.io;
+    const bool weights = io.d_q_weight || io.d_k_weight;
     if (!weights) A.part = nullptr;
     if (A.tokens == 0 && !weights) return HGA_OK;
-    const QkWork K = make_work<T, D>(A.tokens, A.Hq, A.Hkv, A.io.dv ? A.Hkv : 0);
+    QkWork K = {{A.Hq, A.Hkv, io.dv ? A.Hkv : 0}, {}, {}, {}, {A.Hq, A.Hkv, A.Hkv}, {io.q, io.k, nullptr},
+                {io.q_stride, io.k_stride, 0}, {io.d_q, io.d_k, io.d_v}, {io.dq, io.dk, io.dv},
+                {io.dq_stride, io.dk_stride, io.dv_stride}, {}, {io.q_weight, io.k_weight, nullptr}, 1, 0u};
+    set_work(K, Row<T, D>::N, A.tokens);
     // without tokens one CTA writes the weights' zero gradients
-    const int grid = (int)std::max<int64_t>(
-        1, std::min<int64_t>(kGradCtas, (A.tokens * K.split + kWarps - 1) / kWarps));
-    if (A.rope.interleaved) k_qk_grad<T, G, D, true><<<grid, kThreads, 0, st>>>(A, K);
-    else k_qk_grad<T, G, D, false><<<grid, kThreads, 0, st>>>(A, K);
-    const cudaError_t e = cudaGetLastError();
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(kGradCtas, ((int64_t)K.warps + kWarps - 1) / kWarps));
+    auto *k = A.rope.interleaved ? K.split > 1 ? k_qk_grad<T, G, D, true, true> : k_qk_grad<T, G, D, true, false>
+              : K.split > 1      ? k_qk_grad<T, G, D, false, true>
+                                 : k_qk_grad<T, G, D, false, false>;
+    const size_t smem = (size_t)kWarps * kGradDepth * grad_step<T, G>();
+    cudaError_t e = ensure_smem((const void *)k, smem);
+    if (e != cudaSuccess) return cuda_status(e);
+    k<<<grid, kThreads, smem, st>>>(A, K);
+    e = cudaGetLastError();
     if (e != cudaSuccess || !weights) return cuda_status(e);
     return cuda_status(launch_dependent(k_qk_weight_grad<D>, dim3(2 * D / 32), dim3(1024), 0, st,
-                                        (const float *)A.part, grid, A.io.d_q_weight,
-                                        A.io.d_k_weight));
+                                        (const float *)A.part, grid, io.d_q_weight, io.d_k_weight));
 }
 
 }  // namespace
