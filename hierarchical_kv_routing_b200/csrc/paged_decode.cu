@@ -27,14 +27,12 @@
 // 4 KB of V through a ring of kStages in shared memory (cp.async, 16 bytes a
 // lane), three deep, so two CTAs per SM keep 128 KB in flight, above the ~50 KB
 // that 7 TB/s and a microsecond of latency ask for.  The page of each key comes
-// from the block table one tile ahead of its loads.  The warps take every fourth
-// tile of one KV head and are merged in shared memory at an item's end.  (Giving
-// the four warps adjacent heads of the same keys instead, whole runs of a page's
-// token rows, costs four times the parts and was slower: 326 against 317 us at
-// 16 x 64K tokens of 4 heads of 128, 33 against 24 us at 1 x 32K.)
+// from the block table one tile ahead of its loads.  The warps of a KV head take
+// its tiles in turn and are merged in shared memory at an item's end.
 #include <algorithm>
 
 #include "paged_internal.cuh"
+#include "sm100.cuh"
 
 namespace hga {
 
@@ -42,19 +40,26 @@ __device__ int g_paged_error = 0;
 
 namespace {
 
+using sm100::f2_fma;
+using sm100::f2_mul;
+using sm100::f2_pack;
+using sm100::f2_unpack;
+
 constexpr int kWarps = 4, kThreads = kWarps * 32, kStages = 3;
 constexpr int kTileBytes = 4096;             // of K, and of V, per warp and stage
 constexpr int kMaxCtas = 2 * 148;            // two per SM
 constexpr int kUnitTiles = 4;                // tiles of a unit, over the warps of one head
 
 struct Split {
-    int items;         // per sequence: Hkv * gsplit
-    int gsplit, gch;   // chunks of a KV head's query heads, heads (rows) per chunk
-    int n;             // CTAs
+    int items;         // per sequence: Hkv / hw
+    int hw;            // adjacent KV heads of a CTA
+    int gsplit, gch;   // chunks of a KV head's query heads, heads per chunk
+    int rows;          // hw * gch: rows of a CTA's item
+    int n;             // ranges; gsplit CTAs, one per chunk, walk each
     int by_item;       // join entries indexed by item (else by the CTA that starts it)
-    float *part;       // [n][2][gch][D]: continued and opened item, unnormalised
-    float2 *ml;        // [n][2][gch]: running maximum (base 2) and sum
-    int4 *join;        // entry: (sequence, item, first CTA, last CTA); first -1: not split
+    float *part;       // [CTAs][2][rows][D]: continued and opened item, unnormalised
+    float2 *ml;        // [CTAs][2][rows]: running maximum (base 2) and sum
+    int4 *join;        // entry: (sequence, item, first range, last range); first -1: not split
 };
 
 __device__ __forceinline__ uint32_t su32(const void *p) {
@@ -286,18 +291,21 @@ template <int D, int kRows> struct TileBf16 {
     }
 };
 
-// ---- fp32: CUDA cores.  A group of eight lanes takes a key (four keys at a
-// time), each lane 16 bytes of every 128; scores are summed over the group, the
-// weights pass through shared memory, and for P V a lane owns four dimensions
-// (with D = 64 the half-warps take alternate halves of the tile's keys).
+// ---- fp32: CUDA cores, two-lane arithmetic.  A group of eight lanes takes a key
+// (four keys at a time), each lane 16 bytes of every 128, for all rows; the eight
+// lanes' partial scores are summed so that lane i of the group ends with row i's
+// (each step halves the rows a lane keeps: kRows - 1 shuffles instead of 3 kRows),
+// and the softmax of a row is one lane's.  The weights pass through shared memory,
+// doubled for the two-lane products, and for P V a lane owns four dimensions (with
+// D = 64 the half-warps take alternate halves of the tile's keys).
 template <int D, int kRows> struct TileF32 {
     using T = float;
     static constexpr int kKeys = kTileBytes / (D * 4), kSwz = 0, kMerge = 4;
     static constexpr int QC = D / 32, KG = kKeys / 4, LPR = D / 4;   // lanes per V row
     static constexpr int VK = kKeys * LPR / 32;                        // V rows per lane
-    float4 q[kRows][QC];
-    float4 o[kRows];
-    float m[kRows], l[kRows];
+    uint64_t q[kRows][2 * QC];
+    uint64_t o[kRows][2];
+    float m, l;                               // of row lane % kRows
 
     __device__ __forceinline__ void begin(const PagedArgs &A, int b, int head0, int heads) {
         const int lane = threadIdx.x & 31;
@@ -305,118 +313,121 @@ template <int D, int kRows> struct TileF32 {
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
 #pragma unroll
-            for (int i = 0; i < QC; ++i)
-                q[r][i] = r < heads ? *reinterpret_cast<const float4 *>(base + r * D + i * 32 +
-                                                                         (lane & 7) * 4)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-            o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-            m[r] = -INFINITY;
-            l[r] = 0.f;
+            for (int i = 0; i < QC; ++i) {
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < heads) x = *reinterpret_cast<const float4 *>(base + r * D + i * 32 + (lane & 7) * 4);
+                q[r][2 * i] = f2_pack(x.x, x.y);
+                q[r][2 * i + 1] = f2_pack(x.z, x.w);
+            }
+            o[r][0] = o[r][1] = f2_pack(0.f, 0.f);
         }
+        m = -INFINITY;
+        l = 0.f;
     }
 
     __device__ __forceinline__ void tile(uint32_t ks_, uint32_t vs_, uint32_t valid, float scale,
                                          float *ps) {
         const int lane = threadIdx.x & 31, l8 = lane & 7, kg = lane >> 3;
-        const float *ks = static_cast<const float *>(__cvta_shared_to_generic(ks_));
-        const float *vs = static_cast<const float *>(__cvta_shared_to_generic(vs_));
-        float s[KG][kRows];
+        const ulonglong2 *ks = static_cast<const ulonglong2 *>(__cvta_shared_to_generic(ks_));
+        const ulonglong2 *vs = static_cast<const ulonglong2 *>(__cvta_shared_to_generic(vs_));
+        float s[KG];                          // of this lane's row
 #pragma unroll
         for (int k = 0; k < KG; ++k) {
-            float4 x[QC];
+            ulonglong2 x[QC];
 #pragma unroll
-            for (int i = 0; i < QC; ++i)
-                x[i] = *reinterpret_cast<const float4 *>(ks + (k * 4 + kg) * D + i * 32 + l8 * 4);
+            for (int i = 0; i < QC; ++i) x[i] = ks[((k * 4 + kg) * D + i * 32 + l8 * 4) / 4];
+            float a[kRows];
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                float a = 0.f;
+                uint64_t acc = f2_mul(q[r][0], x[0].x);
+                acc = f2_fma(q[r][1], x[0].y, acc);
 #pragma unroll
-                for (int i = 0; i < QC; ++i) {
-                    a = fmaf(q[r][i].x, x[i].x, a);
-                    a = fmaf(q[r][i].y, x[i].y, a);
-                    a = fmaf(q[r][i].z, x[i].z, a);
-                    a = fmaf(q[r][i].w, x[i].w, a);
+                for (int i = 1; i < QC; ++i) {
+                    acc = f2_fma(q[r][2 * i], x[i].x, acc);
+                    acc = f2_fma(q[r][2 * i + 1], x[i].y, acc);
                 }
-                s[k][r] = a;
+                const float2 f = f2_unpack(acc);
+                a[r] = f.x + f.y;
             }
-        }
+            // lane i keeps the rows whose bit agrees with its own, and sends the others
 #pragma unroll
-        for (int k = 0; k < KG; ++k) {
-            const bool live = (valid >> (k * 4 + kg)) & 1u;
+            for (int w = kRows / 2; w > 0; w >>= 1) {
+                const bool up = (l8 & w) != 0;
+#pragma unroll
+                for (int r = 0; r < w; ++r) {
+                    const float send = up ? a[r] : a[r + w], keep = up ? a[r + w] : a[r];
+                    a[r] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+                }
+            }
+#pragma unroll
+            for (int w = kRows; w < 8; w <<= 1) a[0] += __shfl_xor_sync(0xffffffffu, a[0], w);
+            s[k] = (valid >> (k * 4 + kg)) & 1u ? a[0] * scale : -INFINITY;
+        }
+        float top = s[0];
+#pragma unroll
+        for (int k = 1; k < KG; ++k) top = fmaxf(top, s[k]);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        const bool grow = top > m + 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+            const float f = grow ? ex2(m - top) : 1.f;
+            if (grow) m = top;
+            l *= f;
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-                s[k][r] += __shfl_xor_sync(0xffffffffu, s[k][r], 1);
-                s[k][r] += __shfl_xor_sync(0xffffffffu, s[k][r], 2);
-                s[k][r] += __shfl_xor_sync(0xffffffffu, s[k][r], 4);
-                s[k][r] = live ? s[k][r] * scale : -INFINITY;
+                const float fr = __shfl_sync(0xffffffffu, f, r);
+                o[r][0] = f2_mul(o[r][0], f2_pack(fr, fr));
+                o[r][1] = f2_mul(o[r][1], f2_pack(fr, fr));
             }
         }
+        const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            float top = s[0][r];
-#pragma unroll
-            for (int k = 1; k < KG; ++k) top = fmaxf(top, s[k][r]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            if (top > m[r] + 8.f) {            // the same in every lane
-                const float f = ex2(m[r] - top);
-                m[r] = top;
-                l[r] *= f;
-                o[r].x *= f, o[r].y *= f, o[r].z *= f, o[r].w *= f;
-            }
-            const float ref = m[r] == -INFINITY ? 0.f : m[r];
-#pragma unroll
-            for (int k = 0; k < KG; ++k) {
-                const float p = ex2(s[k][r] - ref);
-                l[r] += p;
-                if (l8 == r) ps[r * kKeys + k * 4 + kg] = p;
-            }
+        for (int k = 0; k < KG; ++k) {
+            const float p = ex2(s[k] - ref);
+            l += p;
+            if (l8 < kRows)
+                *reinterpret_cast<float2 *>(ps + (l8 * kKeys + k * 4 + kg) * 2) = make_float2(p, p);
         }
         __syncwarp();
         const int k0 = LPR == 32 ? 0 : (lane / LPR) * VK;
-        float4 x[VK];
 #pragma unroll
-        for (int k = 0; k < VK; ++k)
-            x[k] = *reinterpret_cast<const float4 *>(vs + (k0 + k) * D + (lane % LPR) * 4);
+        for (int k = 0; k < VK; k += 2) {
+            const ulonglong2 x = vs[((k0 + k) * D + (lane % LPR) * 4) / 4];
+            const ulonglong2 y = vs[((k0 + k + 1) * D + (lane % LPR) * 4) / 4];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-            for (int k4 = 0; k4 < VK; k4 += 4) {
-                const float4 p = *reinterpret_cast<const float4 *>(ps + r * kKeys + k0 + k4);
-                const float pk[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    o[r].x = fmaf(pk[j], x[k4 + j].x, o[r].x);
-                    o[r].y = fmaf(pk[j], x[k4 + j].y, o[r].y);
-                    o[r].z = fmaf(pk[j], x[k4 + j].z, o[r].z);
-                    o[r].w = fmaf(pk[j], x[k4 + j].w, o[r].w);
-                }
+            for (int r = 0; r < kRows; ++r) {
+                const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(ps + (r * kKeys + k0 + k) * 2);
+                o[r][0] = f2_fma(p.x, x.x, o[r][0]);
+                o[r][1] = f2_fma(p.x, x.y, o[r][1]);
+                o[r][0] = f2_fma(p.y, y.x, o[r][0]);
+                o[r][1] = f2_fma(p.y, y.y, o[r][1]);
             }
+        }
         __syncwarp();
     }
 
     __device__ __forceinline__ void end() {
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (LPR == 16) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
-            if (LPR == 16) {
-                o[r].x += __shfl_xor_sync(0xffffffffu, o[r].x, 16);
-                o[r].y += __shfl_xor_sync(0xffffffffu, o[r].y, 16);
-                o[r].z += __shfl_xor_sync(0xffffffffu, o[r].z, 16);
-                o[r].w += __shfl_xor_sync(0xffffffffu, o[r].w, 16);
-            }
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 f = f2_unpack(o[r][j]);
+                    o[r][j] = f2_pack(f.x + __shfl_xor_sync(0xffffffffu, f.x, 16),
+                                      f.y + __shfl_xor_sync(0xffffffffu, f.y, 16));
+                }
         }
     }
     __device__ __forceinline__ void put(int round, float *rows, float2 *ml) const {
         const int lane = threadIdx.x & 31;
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
-            if (r / kMerge == round) {
-                if (lane < LPR)
-                    *reinterpret_cast<float4 *>(rows + (r % kMerge) * D + lane * 4) = o[r];
-                if (lane == 0) ml[r % kMerge] = make_float2(m[r], l[r]);
-            }
+            if (r / kMerge == round && lane < LPR)
+                *reinterpret_cast<ulonglong2 *>(rows + (r % kMerge) * D + lane * 4) =
+                    make_ulonglong2(o[r][0], o[r][1]);
+        if (lane < kRows && lane / kMerge == round) ml[lane % kMerge] = make_float2(m, l);
     }
 };
 
@@ -446,12 +457,13 @@ __device__ __forceinline__ void empty_rows(const PagedArgs &A, const Split &S) {
         for (int h = threadIdx.x; A.lse && h < A.Hq; h += kThreads)
             A.lse[(int64_t)b * A.Hq + h] = -INFINITY;
         if (S.by_item)
-            for (int i = threadIdx.x; i < S.items; i += kThreads)
-                S.join[(int64_t)b * S.items + i] = make_int4(0, 0, -1, -1);
+            for (int i = threadIdx.x; i < S.items * S.gsplit; i += kThreads)
+                S.join[(int64_t)b * S.items * S.gsplit + i] = make_int4(0, 0, -1, -1);
     }
 }
 
-template <typename Tile, int D, int kRows>
+// kHw: adjacent KV heads of a CTA; the warps of a head take its tiles in turn.
+template <typename Tile, int D, int kRows, int kHw>
 __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A, const Split S) {
     using T = typename Tile::T;
     constexpr int kKeys = Tile::kKeys, kCpr = D * (int)sizeof(T) / 16, kLoads = kTileBytes / 512;
@@ -460,11 +472,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     __shared__ long long sums[kWarps];
     __shared__ uint32_t valid[kWarps][kStages];
     __shared__ float2 ml[kWarps][Tile::kMerge];
-    __shared__ __align__(16) float ps[sizeof(T) == 4 ? kWarps * kRows * kKeys : 1];
+    __shared__ __align__(16) float ps[sizeof(T) == 4 ? kWarps * kRows * kKeys * 2 : 1];
     float *merge = reinterpret_cast<float *>(ring + kWarps * kStages * 2 * kTileBytes);
 
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+    const int range = cta / S.gsplit, chunk = cta % S.gsplit;
+    const int g0 = chunk * S.gch, heads = min(S.gch, A.G - g0);
+    constexpr int kKw = kWarps / kHw;
+    const int hsub = warp % kHw, ksub = warp / kHw;        // the warp's head, and its tiles
     const int uk = kUnitTiles * kKeys;
     // ---- where this CTA's units begin: sums over runs of sequences, one per thread
     const int per = (A.B + kThreads - 1) / kThreads;
@@ -488,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     // with fewer units than CTAs the last ones take none, so that a split item's
     // parts lie in CTAs without a gap
     const long long n = U < S.n ? U : S.n;
-    const long long u0 = cta < n ? U * cta / n : 0, u1 = cta < n ? U * (cta + 1) / n : 0;
+    const long long u0 = range < n ? U * range / n : 0, u1 = range < n ? U * (range + 1) / n : 0;
     if (u0 < u1 && u0 >= before && u0 < before + mine) {
         long long at = u0 - before;
         for (int b = r0; b < r1; ++b) {
@@ -522,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     const int page_mask = (1 << A.log2_page) - 1;
 
     // ---- producer: the next tile's page entries are read one tile ahead of its rows
-    int pk = P.k0(uk) + warp * kKeys, pk1 = P.k1(uk);
+    int pk = P.k0(uk) + ksub * kKeys, pk1 = P.k1(uk);
     bool plive = true;                              // false: no tile left
     int ptok = 0, ppage = 0, phead = 0;
     bool pin = false;
@@ -532,15 +549,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
                 plive = false;
                 return;
             }
-            pk = P.k0(uk) + warp * kKeys;
+            pk = P.k0(uk) + ksub * kKeys;
             pk1 = P.k1(uk);
         }
         const int key = pk + (lane & (kKeys - 1));
         pin = key < pk1;
         ptok = key < P.v.s ? key : key - P.v.s + P.v.lo;
         ppage = pin ? A.table[(int64_t)P.b * A.max_pages + (ptok >> A.log2_page)] : 0;
-        phead = P.it / S.gsplit;
-        pk += kKeys * kWarps;
+        phead = P.it * kHw + hsub;
+        pk += kKeys * kKw;
     };
     auto issue = [&](int stage) {
         if (plive) {
@@ -575,37 +592,38 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     int4 joined = make_int4(0, 0, -1, -1);
     long long done = 0;                             // units before the segment
     for (;;) {
-        const int k1 = C.k1(uk), h = C.it / S.gsplit, g0 = (C.it % S.gsplit) * S.gch;
-        const int heads = min(S.gch, A.G - g0);
-        t.begin(A, C.b, h * A.G + g0, heads);
-        for (int k = C.k0(uk) + warp * kKeys; k < k1; k += kKeys * kWarps) {
+        const int k1 = C.k1(uk), h0 = C.it * kHw;
+        t.begin(A, C.b, (h0 + hsub) * A.G + g0, heads);
+        for (int k = C.k0(uk) + ksub * kKeys; k < k1; k += kKeys * kKw) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
             __syncwarp();
             issue(stage == 0 ? kStages - 1 : stage - 1);
             const uint32_t ks = ring_s + stage * 2 * kTileBytes;
             t.tile(ks, ks + kTileBytes, valid[warp][stage], A.scale_log2,
-                   ps + (sizeof(T) == 4 ? warp * kRows * kKeys : 0));
+                   ps + (sizeof(T) == 4 ? warp * kRows * kKeys * 2 : 0));
             stage = stage == kStages - 1 ? 0 : stage + 1;
         }
         t.end();
         // ---- the segment's rows: merged over the warps, then out or parked
         const bool cont = C.u > 0, open = C.u + C.cnt < C.nu, whole = !cont && !open;
-        const int64_t row_at = ((int64_t)cta * 2 + (cont ? 0 : 1)) * S.gch;
+        const int64_t row_at = ((int64_t)cta * 2 + (cont ? 0 : 1)) * S.rows;
 #pragma unroll
         for (int round = 0; round < (kRows + Tile::kMerge - 1) / Tile::kMerge; ++round) {
             t.put(round, merge + warp * Tile::kMerge * D, ml[warp]);
             __syncthreads();
-            for (int e = tid; e < Tile::kMerge * (D / 4); e += kThreads) {
-                const int d = (e % (D / 4)) * 4, r = e / (D / 4), row = round * Tile::kMerge + r;
-                if (row >= heads) break;
+            for (int e = tid; e < kHw * Tile::kMerge * (D / 4); e += kThreads) {
+                const int d = (e % (D / 4)) * 4, r = e / (D / 4) % Tile::kMerge;
+                const int hs = e / (D / 4 * Tile::kMerge), row = round * Tile::kMerge + r;
+                if (row >= heads) continue;
                 float top = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][r].x);
+                #pragma unroll
+                for (int k = 0; k < kKw; ++k) top = fmaxf(top, ml[k * kHw + hs][r].x);
                 const float ref = top == -INFINITY ? 0.f : top;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
                 float sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
+                for (int k = 0; k < kKw; ++k) {
+                    const int w = k * kHw + hs;
                     const float f = ex2(ml[w][r].x - ref);
                     const float4 x =
                         *reinterpret_cast<const float4 *>(merge + (w * Tile::kMerge + r) * D + d);
@@ -615,12 +633,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
                 }
                 if (whole) {
                     const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-                    const int64_t at = (int64_t)C.b * A.Hq + h * A.G + g0 + row;
+                    const int64_t at = (int64_t)C.b * A.Hq + (h0 + hs) * A.G + g0 + row;
                     put4<T>(static_cast<T *>(A.out) + at * D + d,
                             make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
                     if (A.lse && d == 0) A.lse[at] = (top + log2f(sum)) * kLn2;
                 } else {
-                    const int64_t at = row_at + row;
+                    const int64_t at = row_at + hs * S.gch + row;
                     *reinterpret_cast<float4 *>(S.part + at * D + d) = a;
                     if (d == 0) S.ml[at] = make_float2(top, sum);
                 }
@@ -629,11 +647,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
         }
         if (!cont) {
             if (open) {
-                // the CTA that holds the item's last unit
+                // the range that holds the item's last unit
                 const long long last = u0 + done + C.nu - 1;
-                joined = make_int4(C.b, C.it, cta, (int)(((last + 1) * n - 1) / U));
+                joined = make_int4(C.b, C.it, range, (int)(((last + 1) * n - 1) / U));
             }
-            if (S.by_item && tid == 0) S.join[(int64_t)C.b * S.items + C.it] = joined;
+            if (S.by_item && tid == 0)
+                S.join[((int64_t)C.b * S.items + C.it) * S.gsplit + chunk] = joined;
         }
         done += C.cnt;
         if (!C.next(A, S, uk)) break;
@@ -658,21 +677,24 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs A, 
     __shared__ float4 acc[kGroups][kLanes];
     __shared__ float sum_s;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int4 j = S.join[blockIdx.x];
     if (j.z < 0) return;
-    const int b = j.x, h = j.y / S.gsplit, g0 = (j.y % S.gsplit) * S.gch;
+    const int chunk = blockIdx.x % S.gsplit, b = j.x, h0 = j.y * S.hw, g0 = chunk * S.gch;
     const int tid = threadIdx.x, cnt = j.w - j.z + 1, heads = min(S.gch, A.G - g0);
     const int lane = tid % kLanes, grp = tid / kLanes;
+    // rows: hw heads of gch query heads, of which `heads` exist
     auto out = [&](int row, float4 a, float top, float sum) {
         const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-        const int64_t to = (int64_t)b * A.Hq + h * A.G + g0 + row;
+        const int64_t to = (int64_t)b * A.Hq + (h0 + row / S.gch) * A.G + g0 + row % S.gch;
         put4<T>(static_cast<T *>(A.out) + to * D + lane * 4,
                 make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
         if (A.lse && lane == 0) A.lse[to] = (top + log2f(sum)) * kLn2;
     };
     if (cnt <= kFew) {
         if (blockIdx.y) return;
-        for (int row = grp; row < heads; row += kGroups) {
+        for (int row = grp; row < S.rows; row += kGroups) {
+            if (row % S.gch >= heads) continue;
             float top = -INFINITY, sum = 0.f;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int i0 = 0; i0 < cnt; i0 += 4) {
@@ -681,7 +703,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs A, 
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int i = i0 + k;
-                    const int64_t at = ((int64_t)(j.z + i) * 2 + (i == 0)) * S.gch + row;
+                    const int64_t at = (((int64_t)(j.z + i) * S.gsplit + chunk) * 2 + (i == 0)) * S.rows + row;
                     x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                     y[k] = make_float2(-INFINITY, 0.f);
                     if (i < cnt) {
@@ -707,8 +729,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs A, 
         return;
     }
     const int row = blockIdx.y;
-    if (row >= heads) return;
-    auto at = [&](int i) { return ((int64_t)(j.z + i) * 2 + (i == 0)) * S.gch + row; };
+    if (row % S.gch >= heads) return;
+    auto at = [&](int i) {
+        return (((int64_t)(j.z + i) * S.gsplit + chunk) * 2 + (i == 0)) * S.rows + row;
+    };
     // the first kAhead parts of a thread are on their way while the weights are formed
     float4 x[kAhead];
 #pragma unroll
@@ -761,43 +785,53 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs A, 
     out(row, a, top, sum_s);
 }
 
-Split make_split(int B, int Hq, int Hkv, int dtype) {
+Split make_split(int B, int Hq, int Hkv, int D, int dtype) {
     Split S = {};
     const int G = Hq / Hkv, most = dtype == HGA_BF16 ? 16 : 8;
+    // Runs of 256 bytes: bf16 heads of 64 are taken in pairs (64 x 16K tokens of 8
+    // heads: 366 us one by one, 320 in pairs); for rows of 256 bytes and more one head
+    // a CTA is faster, as four times the parts cost more than longer runs give (16 x
+    // 64K tokens of 4 heads of 128: 316 us against 326 for four heads).
+    S.hw = D * (dtype == HGA_BF16 ? 2 : 4) < 256 && Hkv % 2 == 0 ? 2 : 1;
+    // More query heads than a tile has rows are cut into chunks; the CTAs of a range's
+    // chunks run side by side, so that the second reads K and V from L2.
     S.gsplit = (G + most - 1) / most;
     S.gch = (G + S.gsplit - 1) / S.gsplit;
     S.gsplit = (G + S.gch - 1) / S.gch;
-    S.items = Hkv * S.gsplit;
-    S.by_item = (long long)B * S.items <= kMaxCtas;
+    S.items = Hkv / S.hw;
+    S.rows = S.hw * S.gch;
+    S.by_item = (long long)B * S.items * S.gsplit <= kMaxCtas;
     return S;
 }
 
+// CTAs of a call at most: two per SM, and at least one range
+inline int max_ctas(const Split &S) { return std::max(kMaxCtas, S.gsplit); }
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-template <typename Tile, int D, int kRows>
+template <typename Tile, int D, int kRows, int kHw>
 hga_status run(const PagedArgs &A, const Split &S, cudaStream_t st) {
-    auto *k = k_paged_decode<Tile, D, kRows>;
+    auto *k = k_paged_decode<Tile, D, kRows, kHw>;
     const size_t smem = smem_bytes<Tile, D>();
     cudaError_t e = ensure_smem((const void *)k, smem);
     if (e != cudaSuccess) return cuda_status(e);
-    k<<<S.n, kThreads, smem, st>>>(A, S);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_status(e);
-    const int entries = S.by_item ? A.B * S.items : S.n;
-    return cuda_status(launch_dependent(k_paged_join<typename Tile::T, D>, dim3(entries, S.gch),
+    e = launch_dependent(k, dim3(S.n * S.gsplit), dim3(kThreads), smem, st, A, S);
+    if (e != cudaSuccess) return cuda_status(e);
+    const int entries = (S.by_item ? A.B * S.items : S.n) * S.gsplit;
+    return cuda_status(launch_dependent(k_paged_join<typename Tile::T, D>, dim3(entries, S.rows),
                                         dim3(kJoinThreads), 0, st, A, S));
 }
 
 }  // namespace
 
 size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int dtype) {
-    const Split S = make_split(B, Hq, Hkv, dtype);
-    const size_t rows = (size_t)kMaxCtas * 2 * S.gch;
-    return up256(rows * D * 4) + up256(rows * sizeof(float2)) + up256(kMaxCtas * sizeof(int4));
+    const Split S = make_split(B, Hq, Hkv, D, dtype);
+    const size_t rows = (size_t)max_ctas(S) * 2 * S.rows;
+    return up256(rows * D * 4) + up256(rows * sizeof(float2)) + up256(max_ctas(S) * sizeof(int4));
 }
 
 hga_status launch_paged_decode(const PagedArgs &A, int dtype, int D, void *ws, cudaStream_t st) {
-    Split S = make_split(A.B, A.Hq, A.Hkv, dtype);
-    const size_t rows = (size_t)kMaxCtas * 2 * S.gch;
+    Split S = make_split(A.B, A.Hq, A.Hkv, D, dtype);
+    const size_t rows = (size_t)max_ctas(S) * 2 * S.rows;
     char *p = static_cast<char *>(ws);
     S.part = reinterpret_cast<float *>(p);
     p += up256(rows * D * 4);
@@ -809,19 +843,22 @@ hga_status launch_paged_decode(const PagedArgs &A, int dtype, int D, void *ws, c
     if (A.window > 0) most = std::min(most, (long long)A.window + A.sinks);
     const int uk = kUnitTiles * (kTileBytes / (D * (dtype == HGA_BF16 ? 2 : 4)));
     const long long units = (most + uk - 1) / uk * S.items * A.B;
-    S.n = (int)std::max(1ll, std::min(units, (long long)std::min(2 * sm_count(), kMaxCtas)));
+    S.n = (int)std::max(1ll, std::min(units, (long long)std::min(2 * sm_count(), kMaxCtas) / S.gsplit));
     if (dtype == HGA_BF16) {
         if (D == 128)
-            return S.gch > 8 ? run<TileBf16<128, 16>, 128, 16>(A, S, st)
-                             : run<TileBf16<128, 8>, 128, 8>(A, S, st);
-        return S.gch > 8 ? run<TileBf16<64, 16>, 64, 16>(A, S, st)
-                         : run<TileBf16<64, 8>, 64, 8>(A, S, st);
+            return S.gch > 8 ? run<TileBf16<128, 16>, 128, 16, 1>(A, S, st)
+                             : run<TileBf16<128, 8>, 128, 8, 1>(A, S, st);
+        if (S.hw == 2)
+            return S.gch > 8 ? run<TileBf16<64, 16>, 64, 16, 2>(A, S, st)
+                             : run<TileBf16<64, 8>, 64, 8, 2>(A, S, st);
+        return S.gch > 8 ? run<TileBf16<64, 16>, 64, 16, 1>(A, S, st)
+                         : run<TileBf16<64, 8>, 64, 8, 1>(A, S, st);
     }
     if (D == 128)
-        return S.gch > 4 ? run<TileF32<128, 8>, 128, 8>(A, S, st)
-                         : run<TileF32<128, 4>, 128, 4>(A, S, st);
-    return S.gch > 4 ? run<TileF32<64, 8>, 64, 8>(A, S, st)
-                     : run<TileF32<64, 4>, 64, 4>(A, S, st);
+        return S.gch > 4 ? run<TileF32<128, 8>, 128, 8, 1>(A, S, st)
+                         : run<TileF32<128, 4>, 128, 4, 1>(A, S, st);
+    return S.gch > 4 ? run<TileF32<64, 8>, 64, 8, 1>(A, S, st)
+                     : run<TileF32<64, 4>, 64, 4, 1>(A, S, st);
 }
 
 hga_status paged_error_take(cudaStream_t st, bool clear) {

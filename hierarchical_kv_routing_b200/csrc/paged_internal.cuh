@@ -76,8 +76,10 @@ hga_status take_error_word(Word &word, cudaStream_t st, bool clear) {
     return (hga_status)v;
 }
 
-// Launch as a programmatic dependent: the grid may start before the kernel
-// before it has ended, and waits (griddepcontrol.wait) before its first read.
+// Launch as a programmatic dependent of whatever precedes on the stream: the grid may
+// start when that kernel's CTAs have all allowed it (or ended), and every kernel
+// launched so waits (griddepcontrol.wait: the kernel before has completed and its
+// writes are visible) before it touches global memory, so only its launch overlaps.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_dependent(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t st, const Args &...args) {

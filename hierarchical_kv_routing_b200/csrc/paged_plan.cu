@@ -91,6 +91,7 @@ __device__ __forceinline__ void fill(const PlanArgs &a, const int32_t *cu, int t
 __global__ void __launch_bounds__(kThreads) k_plan_scan(const PlanArgs a, int fill_here) {
     __shared__ long long part[kWarps + 1];
     __shared__ int32_t ends[kThreads + 1];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lg = a.log2_page, mask = (1 << lg) - 1;
     const long long cap = (long long)a.max_pages << lg;
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(kThreads) k_plan_scan(const PlanArgs a, int fi
 
 __global__ void __launch_bounds__(256) k_plan_fill(const PlanArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int t = blockIdx.x * 256 + threadIdx.x;
     if (t < a.n_slots) fill(a, a.io.cu_tokens, t);
 }
@@ -195,8 +197,8 @@ size_t plan_workspace_bytes(int B, int) { return ((size_t)B * 4 + 255) & ~(size_
 
 hga_status launch_paged_plan(const PlanArgs &a, cudaStream_t st) {
     const bool here = a.n_slots <= kFillHere;
-    k_plan_scan<<<1, kThreads, 0, st>>>(a, here ? 1 : 0);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_dependent(k_plan_scan, dim3(1), dim3(kThreads), 0, st, a, here ? 1 : 0);
     if (e != cudaSuccess || here) return cuda_status(e);
     return cuda_status(launch_dependent(k_plan_fill, dim3((unsigned)((a.n_slots + 255LL) / 256)),
                                         dim3(256), 0, st, a));

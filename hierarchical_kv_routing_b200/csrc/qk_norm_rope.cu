@@ -393,6 +393,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_norm_rope(const QkArgs A, co
     constexpr int P = W::P, N2 = 2 * W::N, E = (int)sizeof(T);
     __shared__ float2 cs_all[kWarps][kMaxHalf];
     extern __shared__ __align__(16) char ring_all[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / W::L;
     const int d0 = (lane % W::L) * W::V;
     const unsigned first = blockIdx.x * (unsigned)kWarps + warp, stride = gridDim.x * kWarps;
@@ -556,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
     constexpr int E = (int)sizeof(T), EG = (int)sizeof(G);
     extern __shared__ __align__(16) char ring_all[];
     __shared__ float2 cs_all[kWarps][kMaxHalf];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / W::L;
     const int d0 = (lane % W::L) * V;
@@ -771,6 +774,7 @@ __global__ void __launch_bounds__(1024) k_qk_weight_grad(const float *part, int 
                                                          float *dkw) {
     __shared__ float red[32][33];
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
     float s = 0.f;
     for (int i = y; i < ctas; i += 32) s += part[(int64_t)i * 2 * D + col];
@@ -816,8 +820,7 @@ template <typename T, int D> hga_status forward(const QkArgs &A, cudaStream_t st
     const size_t smem = (size_t)kWarps * kDepth * kStep;
     const cudaError_t e = ensure_smem((const void *)k, smem);
     if (e != cudaSuccess) return cuda_status(e);
-    k<<<grid, kThreads, smem, st>>>(A, K);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_dependent(k, dim3(grid), dim3(kThreads), smem, st, A, K));
 }
 
 template <typename T, typename G, int D> hga_status backward(const QkGradArgs &A0, cudaStream_t st) {
@@ -838,8 +841,7 @@ template <typename T, typename G, int D> hga_status backward(const QkGradArgs &A
     const size_t smem = (size_t)kWarps * kGradDepth * grad_step<T, G>();
     cudaError_t e = ensure_smem((const void *)k, smem);
     if (e != cudaSuccess) return cuda_status(e);
-    k<<<grid, kThreads, smem, st>>>(A, K);
-    e = cudaGetLastError();
+    e = launch_dependent(k, dim3(grid), dim3(kThreads), smem, st, A, K);
     if (e != cudaSuccess || !weights) return cuda_status(e);
     return cuda_status(launch_dependent(k_qk_weight_grad<D>, dim3(2 * D / 32), dim3(1024), 0, st,
                                         (const float *)A.part, grid, io.d_q_weight, io.d_k_weight));
