@@ -30,6 +30,7 @@
 // from the block table one tile ahead of its loads.  The warps of a KV head take
 // its tiles in turn and are merged in shared memory at an item's end.
 #include <algorithm>
+#include <climits>
 
 #include "paged_internal.cuh"
 #include "sm100.cuh"
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     using T = typename Tile::T;
     constexpr int kKeys = Tile::kKeys, kCpr = D * (int)sizeof(T) / 16, kLoads = kTileBytes / 512;
     extern __shared__ __align__(1024) char ring[];
-    __shared__ int start[3];                       // b, item, unit of the CTA's first unit
+    __shared__ int start[6];       // of the CTA's first unit: b, item, unit; the row's Visible
     __shared__ long long sums[kWarps];
     __shared__ uint32_t valid[kWarps][kStages];
     __shared__ float2 ml[kWarps][Tile::kMerge];
@@ -487,7 +488,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     const int per = (A.B + kThreads - 1) / kThreads;
     const int r0 = min(A.B, tid * per), r1 = min(A.B, r0 + per);
     long long mine = 0;
-    for (int b = r0; b < r1; ++b) mine += (long long)units_of(visible(A, b).n, uk) * S.items;
+    Visible v = {0, 0, 0};
+    for (int b = r0; b < r1; ++b) {
+        v = visible(A, b);
+        mine += (long long)units_of(v.n, uk) * S.items;
+    }
     long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -504,16 +509,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     }
     // with fewer units than CTAs the last ones take none, so that a split item's
     // parts lie in CTAs without a gap
-    const long long n = U < S.n ? U : S.n;
-    const long long u0 = range < n ? U * range / n : 0, u1 = range < n ? U * (range + 1) / n : 0;
+    const int n = U < S.n ? (int)U : S.n;
+    long long u0 = 0, u1 = 0;
+    if (range < n) {
+        // floor(U i / n) = U / n i + (U mod n) i / n, with a 64-bit division only where
+        // the line is that long
+        const bool small = U <= INT_MAX;
+        const long long each = small ? (unsigned)U / (unsigned)n : U / n;
+        const unsigned rest = (unsigned)(U - each * n);
+        u0 = each * range + rest * (unsigned)range / (unsigned)n;
+        u1 = each * (range + 1) + rest * (unsigned)(range + 1) / (unsigned)n;
+    }
     if (u0 < u1 && u0 >= before && u0 < before + mine) {
         long long at = u0 - before;
         for (int b = r0; b < r1; ++b) {
-            const int nu = units_of(visible(A, b).n, uk);
+            if (per > 1) v = visible(A, b);
+            const int nu = units_of(v.n, uk);
             if (at < (long long)nu * S.items) {
                 start[0] = b;
-                start[1] = (int)(at / nu);
-                start[2] = (int)(at % nu);
+                const int it = at <= INT_MAX ? (int)((unsigned)at / (unsigned)nu) : (int)(at / nu);
+                start[1] = it;
+                start[2] = (int)(at - (long long)it * nu);
+                start[3] = v.s, start[4] = v.lo, start[5] = v.n;
                 break;
             }
             at -= (long long)nu * S.items;
@@ -529,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     Walk C;
     C.b = start[0], C.it = start[1], C.u = start[2];
     C.left = u1 - u0;
-    C.v = visible(A, C.b);
+    C.v = {start[3], start[4], start[5]};
     C.nu = units_of(C.v.n, uk);
     C.take();
     Walk P = C;

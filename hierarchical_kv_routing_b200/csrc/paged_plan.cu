@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kFillHere = 8192;   // tokens the scanning CTA fills itself
-constexpr int kRun = 8;           // table entries a thread gives back in a row
+constexpr int kRun = 16;          // table entries a thread gives back at a time
 
 __device__ __forceinline__ void bad() { atomicExch(&g_plan_error, (int)HGA_ERR_BOUNDS); }
 
@@ -62,6 +62,15 @@ __device__ __forceinline__ int find(const int32_t *a, int n, int t) {
     return lo;
 }
 
+// The same over the kThreads rows of `ends` (ends[0] = 0), without a branch, so that
+// several searches run side by side.
+__device__ __forceinline__ int find_row(const int32_t *ends, int e) {
+    int lo = 0;
+#pragma unroll
+    for (int s = kThreads / 2; s > 0; s >>= 1) lo += ends[lo + s] <= e ? s : 0;
+    return lo;
+}
+
 // Slot and position of packed token t, and the table entry if it opens a page.
 // cu: cu_tokens, in shared memory where it fits.
 __device__ __forceinline__ void fill(const PlanArgs &a, const int32_t *cu, int t) {
@@ -91,6 +100,7 @@ __device__ __forceinline__ void fill(const PlanArgs &a, const int32_t *cu, int t
 __global__ void __launch_bounds__(kThreads) k_plan_scan(const PlanArgs a, int fill_here) {
     __shared__ long long part[kWarps + 1];
     __shared__ int32_t ends[kThreads + 1];
+    __shared__ int taken;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lg = a.log2_page, mask = (1 << lg) - 1;
@@ -100,7 +110,8 @@ __global__ void __launch_bounds__(kThreads) k_plan_scan(const PlanArgs a, int fi
         if (tid == 0) bad();
         stack = stack < 0 ? 0 : a.num_pages;
     }
-    // ---- released rows give their pages back
+    // ---- released rows give their pages back: the rows' entries in one line, kRun of
+    // it a thread
     if (a.io.release)
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             const int b = b0 + tid;
@@ -115,32 +126,41 @@ __global__ void __launch_bounds__(kThreads) k_plan_scan(const PlanArgs a, int fi
             __syncthreads();
             const int n = (int)total;
             for (int e0 = 0; e0 < n; e0 += kThreads * kRun) {
-                const int e = e0 + tid * kRun;
-                int ids[kRun], kept = 0, row = e < n ? find(ends, kThreads, e) : 0;
+                // entry e0 + i * kThreads + tid: neighbours in a row are neighbours in the warp
+                int ids[kRun];
+                bool good = true;
 #pragma unroll
                 for (int i = 0; i < kRun; ++i) {
-                    ids[i] = -1;
-                    if (e + i < n) {
-                        while (ends[row + 1] <= e + i) ++row;
-                        ids[i] = a.io.block_table[(int64_t)(b0 + row) * a.max_pages + e + i - ends[row]];
-                        if ((unsigned)ids[i] < (unsigned)a.num_pages) ++kept;
-                        else { ids[i] = -1; bad(); }
-                    }
+                    const int e = min(e0 + i * kThreads + tid, n - 1), row = find_row(ends, e);
+                    ids[i] = a.io.block_table[(int64_t)(b0 + row) * a.max_pages + e - ends[row]];
                 }
-                long long all, at = stack + scan(kept, part, all);
 #pragma unroll
-                for (int i = 0; i < kRun; ++i)
-                    if (ids[i] >= 0) {
-                        if (at < a.num_pages) a.io.free_pages[at] = ids[i];
-                        else bad();
-                        ++at;
-                    }
-                stack = stack + all < a.num_pages ? stack + all : a.num_pages;
+                for (int i = 0; i < kRun; ++i) good &= (unsigned)ids[i] < (unsigned)a.num_pages;
+                const int many = min(n - e0, kThreads * kRun);
+                if (__syncthreads_and(good) && stack + many <= a.num_pages) {
+#pragma unroll
+                    for (int i = 0; i < kRun; ++i)
+                        if (e0 + i * kThreads + tid < n)
+                            a.io.free_pages[stack + i * kThreads + tid] = ids[i];
+                    stack += many;
+                    continue;
+                }
+                // bad ids are left out, and what the stack has no room for
+#pragma unroll
+                for (int i = 0; i < kRun; ++i) {
+                    const bool real = e0 + i * kThreads + tid < n;
+                    const bool ok = real && (unsigned)ids[i] < (unsigned)a.num_pages;
+                    long long all, at = stack + scan(ok ? 1 : 0, part, all);
+                    if (ok && at < a.num_pages) a.io.free_pages[at] = ids[i];
+                    if (real && (!ok || at >= a.num_pages)) bad();
+                    stack = stack + all < a.num_pages ? stack + all : a.num_pages;
+                }
             }
             __syncthreads();
         }
     // ---- tokens and pages of each row
-    long long tokens = 0, pages = 0, taken = 0;
+    long long tokens = 0, pages = 0;
+    if (tid == 0) taken = 0;             // read after the scans' barriers
     for (int b0 = 0; b0 < a.B; b0 += kThreads) {
         const int b = b0 + tid;
         int len = 0, add = 0, given = 0;
@@ -162,8 +182,9 @@ __global__ void __launch_bounds__(kThreads) k_plan_scan(const PlanArgs a, int fi
         pages += total;
         const bool ok = fits && (need == 0 || from + need <= stack);
         given = ok ? add : 0;
-        scan(ok ? need : 0, part, total);
-        taken += total;
+        // the rows served are the first of those that need pages, so what they take
+        // ends where the last of them does
+        if (ok && need) atomicMax(&taken, (int)(from + need));
         if (b < a.B) {
             a.io.lens_out[b] = len + given;
             a.io.granted[b] = given;
@@ -173,6 +194,7 @@ __global__ void __launch_bounds__(kThreads) k_plan_scan(const PlanArgs a, int fi
             if (b0 == 0) ends[tid + 1] = cu;
         }
     }
+    __syncthreads();
     if (tid == 0) {
         a.io.cu_tokens[0] = 0;
         *a.io.free_count_out = (int32_t)(stack - taken);

@@ -10,14 +10,16 @@
 // takes a token's rows N at a time (a step: 512 bytes of rows, 16 lanes to a bf16
 // row of 128), so that cos and sin (64-bit fixed-point angles, sincospif) are formed
 // once a token.  The steps ahead, the next tokens' among them, are on their way to
-// a ring of shared memory (cp.async, 16 bytes a lane): kDepth of them per warp keep
-// 100 KB and more in flight per SM whatever the registers hold.  From there a lane
-// reads V / 2 pairs of its row, both members, so that no value crosses lanes and
-// only the sum of squares does; the arithmetic is two-lane fp32.
+// a ring of shared memory (cp.async, 16 bytes a lane), so that what is in flight does
+// not depend on registers.  From there a lane reads V / 2 pairs of its row, both
+// members, so that no value crosses lanes and only the sum of squares does; the
+// arithmetic is two-lane fp32.
 // Measured, 32K tokens of 32 + 4 + 4 bf16 heads of 128 (671 MB): 144 us with a
 // 16-byte word per lane loaded to registers and partners exchanged by shuffles
 // (bound by issue and shuffle latency), 121 us with whole pairs per lane and four
-// rows in flight per lane, and with the ring the figures at the kernels below.
+// rows in flight per lane, 111 with the ring; the gradient with fp32 dy (1.31 GB) 259,
+// 231 and 193 us (6.8 TB/s).  Heads of 64 in small numbers are bound by issue, by what
+// a token costs before its rows (2 + 1 + 1 heads of 64: 36 us for 32K tokens).
 #include <algorithm>
 
 #include "paged_internal.cuh"
@@ -49,25 +51,27 @@ template <typename T, int D> struct Row {
 // lane to lane is read one lane after the other), and the position of its next token
 // is on its way while this one's rows are worked on.  (Both read at each token's
 // start: 44 us instead of 35 for 8K tokens of 32 + 4 + 4 heads of 128.)
-struct Angles {
-    unsigned long long turn[2];
+template <int D> struct Angles {
+    static constexpr int J = D / 64;      // pairs per lane
+    unsigned long long turn[J];
     __device__ __forceinline__ void begin(const PairRope &r) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) turn[j] = lane + 32 * j < r.R / 2 ? r.turn[lane + 32 * j] : 0;
+        for (int j = 0; j < J; ++j) turn[j] = lane + 32 * j < r.R / 2 ? r.turn[lane + 32 * j] : 0;
     }
     // the angles of position p, times the magnitude -> cs[R / 2]
     __device__ __forceinline__ void form(const PairRope &r, int32_t p, float2 *cs) const {
         const int lane = threadIdx.x & 31;
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (lane + 32 * j >= r.R / 2) continue;
+        for (int j = 0; j < J; ++j) {
             // the angle in turns modulo 1 as a wrapping 64-bit product: exact for any p
             const unsigned long long u = (unsigned long long)(long long)p * turn[j];
             float s, c;
             sincospif((float)(int)(u >> 32) * 0x1p-31f, &s, &c);
-            cs[lane + 32 * j] = make_float2(c * r.magnitude, s * r.magnitude);
+            // pairs outside the rotated part (rate 0) are left as they are
+            const float m = lane + 32 * j < r.R / 2 ? r.magnitude : 1.f;
+            cs[lane + 32 * j] = make_float2(c * m, s * m);
         }
         __syncwarp();
     }
@@ -217,23 +221,23 @@ template <int P>
 __device__ __forceinline__ void trig(const Place &p, const float2 *cs, float (&c)[P], float (&s)[P]) {
 #pragma unroll
     for (int e = 0; e < P; ++e) {
-        const float2 t = p.turns ? cs[p.pair + e] : make_float2(1.f, 0.f);
+        const float2 t = cs[p.pair + e];
         c[e] = t.x;
         s[e] = t.y;
     }
 }
 
+// A lane's weights as they lie in memory; ones where there are none.
 template <typename T, int P, bool kInter>
-__device__ __forceinline__ Pairs<P> load_weight(const void *w, const Place &p) {
-    Raw<T, P> x;
+__device__ __forceinline__ void load_weight(Raw<T, P> &x, const void *w, const Place &p) {
     if (w) {
         load_raw<T, P, kInter>(x, static_cast<const T *>(w), p, true);
-        return unpack<T, P, kInter>(x);
+        return;
     }
     Pairs<P> y;
 #pragma unroll
     for (int i = 0; i < P / 2; ++i) y.a[i] = y.b[i] = f2_pack(1.f, 1.f);
-    return y;
+    x = pack<T, P, kInter>(y);
 }
 
 template <int L> __device__ __forceinline__ float row_sum(float x) {
@@ -264,18 +268,41 @@ struct QkWork {
     unsigned warps;            // tokens * split: below 2^31, as only few tokens are split
 };
 
-// A warp's walk over the rows of its tokens, a step of N rows at a time.  With
-// kSplit, several warps share a token and each takes the steps [s0, s1) of the
-// kinds' steps in a row.  The first `full` steps left of a kind have all their
-// rows; a last one may be ragged.
-template <int N, bool kSplit> struct Walk {
-    unsigned wg, stride, tok;
-    int kind, left, full;      // kind 3: none left
-    int h;                     // first row (0 without kSplit)
+// The token of warp wg and, of each kind, its steps [a, b): all of them without
+// kSplit; else the warps of a token share the kinds' steps in a row.
+template <bool kSplit> struct Part {
+    unsigned tok;
     int s0, s1;
+    __device__ __forceinline__ void of(const QkWork &K, unsigned wg) {
+        tok = wg;
+        if (kSplit) {
+            const unsigned all = (unsigned)(K.steps[0] + K.steps[1] + K.steps[2]);
+            const unsigned part = wg % (unsigned)K.split;
+            tok = wg / (unsigned)K.split;
+            s0 = (int)(all * part / (unsigned)K.split);
+            s1 = (int)(all * (part + 1) / (unsigned)K.split);
+        }
+    }
+    __device__ __forceinline__ int a(const QkWork &K, int kind) const {
+        return kSplit ? max(s0 - at(K, kind), 0) : 0;
+    }
+    __device__ __forceinline__ int b(const QkWork &K, int kind) const {
+        return kSplit ? min(s1 - at(K, kind), K.steps[kind]) : K.steps[kind];
+    }
+    __device__ __forceinline__ int at(const QkWork &K, int kind) const {
+        return kind == 0 ? 0 : kind == 1 ? K.steps[0] : K.steps[0] + K.steps[1];
+    }
+};
+
+// The walk that runs ahead: the rows of a warp's tokens, a step of N rows at a time.
+// The first `full` steps left of a kind have all their rows; a last one may be ragged.
+template <int N, bool kSplit> struct Walk {
+    unsigned wg, stride;
+    Part<kSplit> part;
+    int kind, left, full;      // kind 3: none left
+    int h;                     // first row
     __device__ __forceinline__ void begin(const QkWork &K, unsigned first, unsigned stride_) {
         wg = first, stride = stride_;
-        h = 0;
         kind = 2;
         next(K);
     }
@@ -287,27 +314,15 @@ template <int N, bool kSplit> struct Walk {
                     kind = 3, left = 0;
                     return;
                 }
-                tok = wg;
-                if (kSplit) {
-                    const unsigned all = (unsigned)(K.steps[0] + K.steps[1] + K.steps[2]);
-                    const unsigned part = wg % (unsigned)K.split;
-                    tok = wg / (unsigned)K.split;
-                    s0 = (int)(all * part / (unsigned)K.split);
-                    s1 = (int)(all * (part + 1) / (unsigned)K.split);
-                }
+                part.of(K, wg);
                 wg += stride;
                 kind = -1;
             }
             ++kind;
-            left = K.steps[kind];
-            full = K.full[kind];
-            if (kSplit) {
-                const int at = kind == 0 ? 0 : kind == 1 ? K.steps[0] : K.steps[0] + K.steps[1];
-                const int a = max(s0 - at, 0), b = min(s1 - at, left);
-                h = a * N;
-                left = b - a;
-                full = min(b, full) - a;
-            }
+            const int a = part.a(K, kind), b = part.b(K, kind);
+            h = a * N;
+            left = b - a;
+            full = (kSplit ? min(b, K.full[kind]) : K.full[kind]) - a;
             if (left > 0) return;
         }
     }
@@ -315,6 +330,12 @@ template <int N, bool kSplit> struct Walk {
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// the same for data that L2 need not keep
+__device__ __forceinline__ void cp16_once(uint32_t dst, const void *src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "l"(policy)
+                 : "memory");
 }
 // zeros, and no read, where live is false
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
@@ -327,9 +348,13 @@ template <int N> __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// ---- forward: steps of 2 N rows (1 KB); 128 registers and 64 KB of ring a CTA, two
-// CTAs per SM.
-constexpr int kDepth = 8, kStep = 1024, kCtas = 148 * 2;
+// ---- forward: steps of 2 N rows (1 KB); 128 registers and 24 KB of ring a CTA, two
+// CTAs per SM.  Half of the traffic is writes, and what bounds the pass is how HBM
+// takes both: more loads in flight make it slower (32K tokens of 32 + 4 + 4 bf16 heads
+// of 128: depth 8 126 us, 3 118; 2 is worse for small heads), and telling L2 that
+// what is read is not read again gives 111 (a plain copy of these 671 MB takes 103).
+// For the gradient, three quarters reads, the hint is worse (217 us for 193).
+constexpr int kDepth = 3, kStep = 1024, kCtas = 148 * 2;
 
 // Two rows of a lane (at lo/hi and 512 bytes on in shared memory, N rows on in
 // memory): y = r (x A + x' B), to `to` and, where given, `also`.
@@ -404,20 +429,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_norm_rope(const QkArgs A, co
     const uint32_t lo = ring + (sub * D + pl.lo) * E, hi = ring + (sub * D + pl.hi) * E;
     const float eps = (float)A.io.eps;
 
+    const uint64_t once = sm100::l2_policy_evict_first();
+
     // ---- the steps ahead
     Walk<N2, kSplit> p = {};
     const T *src = nullptr;
     auto find = [&]() {
         if (p.kind == 3) return;
-        src = static_cast<const T *>(K.in[p.kind]) + p.tok * K.in_stride[p.kind] + (p.h + sub) * D + d0;
+        src = static_cast<const T *>(K.in[p.kind]) + p.part.tok * K.in_stride[p.kind] + (p.h + sub) * D + d0;
     };
     p.begin(K, first, stride);
     find();
     auto issue = [&](uint32_t at) {               // at: offset of a ring slot
         if (p.left > 0) {
             if (p.full > 0) {
-                cp16(mine + at, src);
-                cp16(mine + at + 512, src + W::N * D);
+                cp16_once(mine + at, src, once);
+                cp16_once(mine + at + 512, src + W::N * D, once);
                 --p.full;
             } else {
                 // rows beyond the last are zeros; the address given for them is row 0's
@@ -438,10 +465,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_norm_rope(const QkArgs A, co
     for (int i = 0; i < kDepth - 1; ++i) issue(i * kStep);
 
     // ---- the rows at hand
-    Walk<N2, kSplit> c = {};
-    c.begin(K, first, stride);
-    Angles ang;
+    Angles<D> ang;
     ang.begin(A.rope);
+    Raw<T, P> wraw[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_weight<T, P, kInter>(wraw[i], K.weight[i], pl);
     int32_t next_pos = 0, next_row = -1;          // of the token that comes next
     auto ahead = [&](unsigned wg) {
         if (wg >= K.warps) return;
@@ -450,8 +478,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_norm_rope(const QkArgs A, co
         if (A.io.slot) next_row = A.io.slot[t];
     };
     ahead(first);
-    unsigned tok = ~0u;
-    int page_row = -1;
     uint32_t at = 0, to_fill = (kDepth - 1) * kStep;     // ring offsets
     auto step = [&]() {                           // makes the next step's rows readable
         __syncwarp();                             // the slot filled now has been read
@@ -461,80 +487,86 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_norm_rope(const QkArgs A, co
         __syncwarp();
     };
     auto done = [&]() { at = at == (kDepth - 1) * kStep ? 0 : at + kStep; };
-    for (; c.kind < 3; c.next(K)) {
-        if (c.tok != tok) {                       // a new token: its angles and its slot
-            tok = c.tok;
-            const int32_t pos = next_pos;
-            page_row = next_row;
-            ahead(c.wg);
-            if (A.rope.R && c.kind < 2) ang.form(A.rope, pos, cs);
-            if (page_row < -1 || page_row >= A.io.num_slots) {
-                if (A.io.slot && lane == 0) atomicExch(&g_qk_error, (int)HGA_ERR_BOUNDS);
-                page_row = -1;
-            }
+    if (A.rope.R == 0) ang.form(A.rope, 0, cs);   // rates of 0: cos 1, sin 0
+    for (unsigned wg = first; wg < K.warps; wg += stride) {
+        Part<kSplit> c;
+        c.of(K, wg);
+        const unsigned tok = c.tok;
+        const int32_t pos = next_pos;
+        int page_row = next_row;
+        ahead(wg + stride);
+        if (page_row < -1 || page_row >= A.io.num_slots) {
+            if (A.io.slot && lane == 0) atomicExch(&g_qk_error, (int)HGA_ERR_BOUNDS);
+            page_row = -1;
         }
-        // where the rows go: `to`, and `also` where both are wanted
-        const int rest = K.rest[c.kind], off = (c.h + sub) * D + (c.kind == 2 ? d0 : pl.lo);
-        void *pages = page_row < 0 ? nullptr : K.pages[c.kind];
-        T *to = static_cast<T *>(K.out[c.kind]);
-        T *also = static_cast<T *>(pages);
-        if (to) to += tok * (int64_t)(K.H[c.kind] * D) + off;
-        if (also) also += page_row * (int64_t)(K.H[c.kind] * D) + off;
-        if (!to) to = also, also = nullptr;
-        if (!to) {                                // nowhere: read and dropped
-            for (int n = c.left; n > 0; --n) {
-                step();
-                done();
+        if (A.rope.R && (!kSplit || c.s0 < K.steps[0] + K.steps[1])) ang.form(A.rope, pos, cs);
+#pragma unroll
+        for (int kind = 0; kind < 3; ++kind) {
+            const int first_step = c.a(K, kind), last_step = c.b(K, kind);
+            if (first_step >= last_step) continue;
+            const int rest = K.rest[kind], off = (first_step * N2 + sub) * D + (kind == 2 ? d0 : pl.lo);
+            const bool live0 = sub < rest, live1 = sub + W::N < rest;   // of a ragged last step
+            int full = (kSplit ? min(last_step, K.full[kind]) : K.full[kind]) - first_step;
+            const int ragged = last_step - first_step - full;
+            // where the rows go: `to`, and `also` where both are wanted
+            void *pages = page_row < 0 ? nullptr : K.pages[kind];
+            T *to = static_cast<T *>(K.out[kind]), *also = static_cast<T *>(pages);
+            if (to) to += tok * (int64_t)(K.H[kind] * D) + off;
+            if (also) also += page_row * (int64_t)(K.H[kind] * D) + off;
+            if (!to) to = also, also = nullptr;
+            if (!to) {                            // nowhere: read and dropped
+                for (int n = full + ragged; n > 0; --n) {
+                    step();
+                    done();
+                }
+                continue;
             }
-            continue;
-        }
-        const bool live0 = sub < rest, live1 = sub + W::N < rest;   // of a ragged last step
-        if (c.kind == 2) {                        // values: copied
-            for (int n = c.left; n > 0; --n, --c.full) {
+            if (kind == 2) {                      // values: copied
+                for (int n = full + ragged; n > 0; --n, --full) {
+                    step();
+                    const uint4 x = lds128(mine + at), y = lds128(mine + at + 512);
+                    done();
+                    if (full > 0 || live0) {
+                        *reinterpret_cast<uint4 *>(to) = x;
+                        if (also) *reinterpret_cast<uint4 *>(also) = x;
+                    }
+                    if (full > 0 || live1) {
+                        *reinterpret_cast<uint4 *>(to + W::N * D) = y;
+                        if (also) *reinterpret_cast<uint4 *>(also + W::N * D) = y;
+                    }
+                    to += N2 * D;
+                    if (also) also += N2 * D;
+                }
+                continue;
+            }
+            const bool norm = K.weight[kind] != nullptr;
+            Pairs<P> ct, st;                      // w_a cos, w_b cos; -w_b sin, w_a sin
+            {
+                float cf[P], tf[P];
+                trig<P>(pl, cs, cf, tf);
+                const Pairs<P> w = unpack<T, P, kInter>(wraw[kind]);
+#pragma unroll
+                for (int i = 0; i < P / 2; ++i) {
+                    const uint64_t cc = f2_pack(cf[2 * i], cf[2 * i + 1]);
+                    ct.a[i] = f2_mul(w.a[i], cc);
+                    ct.b[i] = f2_mul(w.b[i], cc);
+                    st.a[i] = f2_mul(w.b[i], f2_pack(-tf[2 * i], -tf[2 * i + 1]));
+                    st.b[i] = f2_mul(w.a[i], f2_pack(tf[2 * i], tf[2 * i + 1]));
+                }
+            }
+            const int skip = pl.hi - pl.lo;
+            for (int n = full; n > 0; --n) {
                 step();
-                const uint4 x = lds128(mine + at), y = lds128(mine + at + 512);
+                two_rows<T, D, kInter, false>(lo + at, hi + at, norm, eps, ct, st, to, also, skip, true, true);
                 done();
-                if (c.full > 0 || live0) {
-                    *reinterpret_cast<uint4 *>(to) = x;
-                    if (also) *reinterpret_cast<uint4 *>(also) = x;
-                }
-                if (c.full > 0 || live1) {
-                    *reinterpret_cast<uint4 *>(to + W::N * D) = y;
-                    if (also) *reinterpret_cast<uint4 *>(also + W::N * D) = y;
-                }
                 to += N2 * D;
                 if (also) also += N2 * D;
             }
-            continue;
-        }
-        const void *weight = K.weight[c.kind];
-        const bool norm = weight != nullptr;
-        Pairs<P> ct, st;                          // w_a cos, w_b cos; -w_b sin, w_a sin
-        {
-            float cf[P], tf[P];
-            trig<P>(pl, cs, cf, tf);
-            const Pairs<P> w = load_weight<T, P, kInter>(weight, pl);
-#pragma unroll
-            for (int i = 0; i < P / 2; ++i) {
-                const uint64_t cc = f2_pack(cf[2 * i], cf[2 * i + 1]);
-                ct.a[i] = f2_mul(w.a[i], cc);
-                ct.b[i] = f2_mul(w.b[i], cc);
-                st.a[i] = f2_mul(w.b[i], f2_pack(-tf[2 * i], -tf[2 * i + 1]));
-                st.b[i] = f2_mul(w.a[i], f2_pack(tf[2 * i], tf[2 * i + 1]));
+            if (ragged) {
+                step();
+                two_rows<T, D, kInter, true>(lo + at, hi + at, norm, eps, ct, st, to, also, skip, live0, live1);
+                done();
             }
-        }
-        const int skip = pl.hi - pl.lo, ragged = c.left - c.full;
-        for (int n = c.full; n > 0; --n) {
-            step();
-            two_rows<T, D, kInter, false>(lo + at, hi + at, norm, eps, ct, st, to, also, skip, true, true);
-            done();
-            to += N2 * D;
-            if (also) also += N2 * D;
-        }
-        if (ragged) {
-            step();
-            two_rows<T, D, kInter, true>(lo + at, hi + at, norm, eps, ct, st, to, also, skip, live0, live1);
-            done();
         }
     }
     cp_wait<0>();
@@ -580,9 +612,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
         if (p.kind == 3) return;
         has_x = K.weight[p.kind] != nullptr;
         if (has_x)
-            src = static_cast<const T *>(K.in[p.kind]) + p.tok * K.in_stride[p.kind] + (p.h + sub) * D + d0;
+            src = static_cast<const T *>(K.in[p.kind]) + p.part.tok * K.in_stride[p.kind] + (p.h + sub) * D + d0;
         gsrc = static_cast<const char *>(K.grad[p.kind]) +
-               (p.tok * (int64_t)(K.H[p.kind] * D) + (p.h + sub) * D) * EG + (lane % W::L) * 16;
+               (p.part.tok * (int64_t)(K.H[p.kind] * D) + (p.h + sub) * D) * EG + (lane % W::L) * 16;
     };
     const uint32_t xto = ring + lane * 16, gto = ring + 512 + sub * D * EG + (lane % W::L) * 16;
     p.begin(K, first, stride);
@@ -616,23 +648,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
 #pragma unroll
     for (int i = 0; i < kGradDepth - 1; ++i) issue(i * S);
 
-    const Pairs<P> wq = load_weight<T, P, kInter>(A.io.q_weight, pl),
-                   wk = load_weight<T, P, kInter>(A.io.k_weight, pl);
+    Raw<T, P> wraw[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_weight<T, P, kInter>(wraw[i], K.weight[i], pl);
     Pairs<P> sumq, sumk;
 #pragma unroll
     for (int e = 0; e < P / 2; ++e) sumq.a[e] = sumq.b[e] = sumk.a[e] = sumk.b[e] = f2_pack(0.f, 0.f);
 
     // ---- the rows at hand
-    Walk<W::N, kSplit> c = {};
-    c.begin(K, first, stride);
-    Angles ang;
+    Angles<D> ang;
     ang.begin(A.rope);
     int32_t next_pos = 0;                         // of the token that comes next
     auto ahead = [&](unsigned wg) {
         if (wg < K.warps && A.rope.R) next_pos = A.io.pos[kSplit ? wg / (unsigned)K.split : wg];
     };
     ahead(first);
-    unsigned tok = ~0u;
     uint32_t at = 0, to_fill = (kGradDepth - 1) * S;     // ring offsets
     auto step = [&]() {                           // makes the next step's rows readable
         __syncwarp();                             // the slot filled now has been read
@@ -691,20 +721,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
         done();
         if (live) store_raw<T, P, kInter>(out, out + (pl.hi - pl.lo), pack<T, P, kInter>(g));
     };
-    auto rows = [&](const Pairs<P> &w, bool norm, T *out, int rest, Pairs<P> &sum) {
-        const int ragged = c.left - c.full;
-        for (int n = c.full; n > 0; --n) {
-            row(w, norm, out, true, sum);
-            out += W::N * D;
-        }
-        if (ragged) row(w, norm, out, sub < rest, sum);
-    };
-    for (; c.kind < 3; c.next(K)) {
-        if (c.tok != tok) {
-            tok = c.tok;
-            const int32_t pos = next_pos;
-            ahead(c.wg);
-            if (A.rope.R && c.kind < 2) ang.form(A.rope, pos, cs);
+    if (A.rope.R == 0) ang.form(A.rope, 0, cs);   // rates of 0: cos 1, sin 0
+    for (unsigned wg = first; wg < K.warps; wg += stride) {
+        Part<kSplit> c;
+        c.of(K, wg);
+        const unsigned tok = c.tok;
+        const int32_t pos = next_pos;
+        ahead(wg + stride);
+        if (A.rope.R && (!kSplit || c.s0 < K.steps[0] + K.steps[1])) ang.form(A.rope, pos, cs);
+        {
             float cf[P], tf[P];
             trig<P>(pl, cs, cf, tf);
 #pragma unroll
@@ -714,15 +739,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
                 tn[e] = f2_pack(-tf[2 * e], -tf[2 * e + 1]);
             }
         }
-        T *out = static_cast<T *>(K.out[c.kind]) + tok * K.out_stride[c.kind] + (c.h + sub) * D;
-        const int rest = K.rest[c.kind];
-        if (c.kind == 0) {
-            rows(wq, K.weight[0] != nullptr, out + pl.lo, rest, sumq);
-        } else if (c.kind == 1) {
-            rows(wk, K.weight[1] != nullptr, out + pl.lo, rest, sumk);
-        } else {                                  // values: rounded to the inputs' type
-            out += d0;
-            for (int n = c.left; n > 0; --n, --c.full) {
+#pragma unroll
+        for (int kind = 0; kind < 3; ++kind) {
+            const int first_step = c.a(K, kind), last_step = c.b(K, kind);
+            if (first_step >= last_step) continue;
+            int full = (kSplit ? min(last_step, K.full[kind]) : K.full[kind]) - first_step;
+            const int ragged = last_step - first_step - full;
+            const bool exists = sub < K.rest[kind];       // the row of a ragged last step
+            T *out = static_cast<T *>(K.out[kind]) + tok * K.out_stride[kind] +
+                     (first_step * W::N + sub) * D + (kind == 2 ? d0 : pl.lo);
+            if (kind < 2) {
+                const Pairs<P> w = unpack<T, P, kInter>(wraw[kind]);
+                const bool norm = K.weight[kind] != nullptr;
+                for (; full > 0; --full) {
+                    row(w, norm, out, true, kind ? sumk : sumq);
+                    out += W::N * D;
+                }
+                if (ragged) row(w, norm, out, exists, kind ? sumk : sumq);
+                continue;
+            }
+            for (int n = full + ragged; n > 0; --n, --full) {   // values: rounded to T
                 step();
                 uint4 raw[GW];
 #pragma unroll
@@ -730,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
                 done();
                 float g[V];
                 unpack_words<G, V>(raw, g);
-                if (c.full > 0 || sub < rest) store_slice<T, V>(out, g);
+                if (full > 0 || exists) store_slice<T, V>(out, g);
                 out += W::N * D;
             }
         }
