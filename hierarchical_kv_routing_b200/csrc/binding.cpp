@@ -54,12 +54,11 @@ inline bool none(PyObject *o) { return o == Py_None; }
 // What a call works on: its device, stream and element type.
 struct Call {
     int dev;
-    PyObject *stream_arg;
     void *stream;
     c10::optional<c10::cuda::CUDAStream> other;   // a given stream
     c10::cuda::OptionalCUDAGuard guard;
 
-    Call(const at::Tensor &t, PyObject *stream_obj) : dev(t.get_device()), stream_arg(stream_obj) {
+    Call(const at::Tensor &t, PyObject *stream_obj) : dev(t.get_device()) {
         if (none(stream_obj)) {
             stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
         } else {
@@ -79,12 +78,13 @@ struct Call {
         if (x == -1 && PyErr_Occurred()) throw Raised();
         return x;
     }
+    // A new tensor, of the given stream's memory: blocks that the current stream has
+    // freed may still be written to by what is queued there.
     at::Tensor empty(at::IntArrayRef shape, at::ScalarType dt) const {
-        at::Tensor t = at::empty(shape, at::TensorOptions().dtype(dt).device(
-                                            at::Device(at::kCUDA, (c10::DeviceIndex)dev)));
-        // the caller may free it before `stream` is done with it
-        if (other) t.record_stream(other->unwrap());
-        return t;
+        const auto options = at::TensorOptions().dtype(dt).device(at::Device(at::kCUDA, (c10::DeviceIndex)dev));
+        if (!other) return at::empty(shape, options);
+        const c10::cuda::CUDAStreamGuard on(*other);
+        return at::empty(shape, options);
     }
 };
 

@@ -15,7 +15,8 @@ A serving step of a layer that attends over every cached token (or a window):
 As in the rest of the package, these functions check their tensors, pass pointers
 to the C ABI and raise HGAError on a refusal; they never synchronise.  The checks
 and the marshalling are compiled (csrc/binding.cpp, module _paged).  With `stream`,
-tensors that a call allocates are recorded on that stream.
+tensors that a call allocates belong to that stream, as if allocated under
+torch.cuda.stream(stream).
 """
 from __future__ import annotations
 

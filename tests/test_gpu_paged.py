@@ -138,6 +138,41 @@ def test_plan_bad_values_are_reported(hga):
     assert hga.hga_device_status() == 5 and hga.hga_device_status() == 0
 
 
+@pytest.mark.parametrize("bad", [0, 1, 40])
+def test_plan_releases_long_rows(hga, bad):
+    """More pages given back than one sweep of the scanning CTA, some ids bad: the good
+    ones lie on the stack in order."""
+    rng = np.random.default_rng(bad)
+    B, page, M = 9, 2, 4000
+    lens = rng.integers(page * M * 3 // 4, page * M, B)
+    held = -(-lens // page)
+    P = int(held.sum()) + 50
+    ids = rng.permutation(P)
+    table, at = np.full((B, M), -1), 0
+    for b in range(B):
+        table[b, :held[b]] = ids[at:at + held[b]]
+        at += held[b]
+    free = np.full(P, -7)
+    free[:50] = ids[at:]
+    release = np.ones(B, int)
+    release[4] = 0
+    if not bad:
+        check_plan(hga, lens, rng.integers(0, 9, B), table, free, 50, page, 100, release)
+        assert hga.hga_device_status() == 0
+        return
+    for _ in range(bad):
+        table[rng.integers(0, B), rng.integers(0, M * 3 // 4)] = rng.choice([-1, P, 2 ** 31 - 1, -2 ** 31])
+    want = free[:50].tolist()
+    for b in range(B):
+        if release[b]:
+            want += [x for x in table[b, :held[b]].tolist() if 0 <= x < P]
+    tf = i32(free)
+    r = hga.hga_paged_plan(i32(lens), i32([0] * B), tf, i32([50]), i32(table), page, 0, release=i32(release))
+    assert r["free_count"].tolist() == [len(want)] and tf[:len(want)].tolist() == want
+    bads = sum(not 0 <= x < P for b in range(B) if release[b] for x in table[b, :held[b]])
+    assert hga.hga_device_status() == (5 if bads else 0)
+
+
 # ------------------------------------------------------------- rotation --
 
 ROPES = [
@@ -585,6 +620,101 @@ def test_captured_step_follows_the_lengths(hga):
         for a, b in zip(vars(eager[0]).values(), vars(graphed[0]).values()):
             assert not isinstance(a, torch.Tensor) or torch.equal(a, b)
     assert hga.hga_device_status() == 0
+
+
+def test_allocations_of_another_stream_do_not_wait_for_this_one(hga):
+    """With `stream`, a call's new tensors come from that stream's memory: a block that
+    the current stream has freed but still writes to is not handed out."""
+    _, q, k, v = qkv(1, 1024, 8, 2, 64, "bf16")
+    pos = i32(np.arange(1024))
+    want = hga.hga_qk_norm_rope(q, k, v, pos, hga.HGARope())
+    kp, vp, table = pages_for(1, [200] * 64, 2, 64, "bf16", 16)
+    qd, lens = queries(1, 64, 64, 64, "bf16"), i32([200] * 64)
+    dec = hga.hga_paged_decode(qd, kp, vp, table, lens)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for op, ref_out in ((lambda: hga.hga_qk_norm_rope(q, k, v, pos, hga.HGARope(), stream=side), want),
+                        (lambda: (hga.hga_paged_decode(qd, kp, vp, table, lens, stream=side),), (dec,))):
+        late = [torch.empty_like(t) for t in ref_out]
+        torch.cuda._sleep(200_000_000)
+        for t in late:
+            t.fill_(7.0)
+        del late, t
+        got = op()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref_out))
+
+
+def test_binding_refusals(hga):
+    """Tensors of the wrong kind are refused with a message before anything runs."""
+    rope = hga.HGARope()
+    x, q, k, v = qkv(1, 6, 4, 2, 64, "bf16")
+    pos = i32(np.arange(6))
+    kp, vp, table = pages_for(1, [20, 3], 2, 64, "bf16", 16)
+    qd, lens = queries(1, 2, 4, 64, "bf16"), i32([20, 3])
+    d = [torch.zeros(6, h, 64, device="cuda") for h in (4, 2, 2)]
+    slot = i32(np.arange(6))
+    cases = [
+        lambda: hga.hga_qk_norm_rope(q.cpu(), k, v, pos, rope),
+        lambda: hga.hga_qk_norm_rope(q.half(), k.half(), v.half(), pos, rope),
+        lambda: hga.hga_qk_norm_rope(q, k.float(), v, pos, rope),
+        lambda: hga.hga_qk_norm_rope(q, k[:5], v, pos, rope),
+        lambda: hga.hga_qk_norm_rope(q[..., :32], k[..., :32], None, pos, hga.HGARope(0)),
+        lambda: hga.hga_qk_norm_rope(q[:, ::2], k, v, pos, rope),
+        lambda: hga.hga_qk_norm_rope(q[:1].expand(6, 4, 64), k, v, pos, rope),
+        lambda: hga.hga_qk_norm_rope(q.transpose(-1, -2), k, v, pos, rope),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos.long(), rope),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos[:5], rope),
+        lambda: hga.hga_qk_norm_rope(q, k, v, None, rope),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos, rope, q_weight=torch.ones(64, device="cuda")),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos, rope, k_pages=kp, slot=slot),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos, rope, k_pages=kp, v_pages=vp),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos, rope, k_pages=kp, v_pages=vp.float(), slot=slot),
+        lambda: hga.hga_qk_norm_rope(q, k, None, pos, rope, v_out=d[1]),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos, rope, q_out=d[0]),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos, rope, eps=-1.0),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos, rope._replace(layout="neox")),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos, rope._replace(scaling="ntk")),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos, rope._replace(rotary_dim=24)),
+        lambda: hga.hga_qk_norm_rope(q, k, v, pos, "half"),
+        lambda: hga.hga_qk_norm_rope(q.unflatten(0, (2, 3)), k, v, pos, rope),
+        lambda: hga.hga_qk_norm_rope_backward(q, k, d[0].half(), d[1].half(), pos, rope),
+        lambda: hga.hga_qk_norm_rope_backward(q, k, d[0], d[1].bfloat16(), pos, rope),
+        lambda: hga.hga_qk_norm_rope_backward(q, k, d[0], d[1], pos, rope, dv=d[2]),
+        lambda: hga.hga_qk_norm_rope_backward(q, k, d[0], d[1], pos, rope, dq=d[0]),
+        lambda: hga.hga_qk_norm_rope_backward(q, k, d[0], d[1], pos, rope,
+                                              workspace=torch.empty(8, device="cuda"),
+                                              q_weight=torch.ones(64, device="cuda").bfloat16()),
+        lambda: hga.hga_paged_decode(qd.float(), kp, vp, table, lens),
+        lambda: hga.hga_paged_decode(qd[:, ::2], kp, vp, table, lens),
+        lambda: hga.hga_paged_decode(qd, kp, vp[:1], table, lens),
+        lambda: hga.hga_paged_decode(qd, kp.transpose(1, 2), vp.transpose(1, 2), table, lens),
+        lambda: hga.hga_paged_decode(qd, kp, vp, table.t(), lens),
+        lambda: hga.hga_paged_decode(qd, kp, vp, table, lens.long()),
+        lambda: hga.hga_paged_decode(qd, kp, vp, table, lens[:1]),
+        lambda: hga.hga_paged_decode(qd[:, :3], kp, vp, table, lens),
+        lambda: hga.hga_paged_decode(qd, kp, vp, table, lens, window=-1),
+        lambda: hga.hga_paged_decode(qd, kp, vp, table, lens, window=1 << 31),
+        lambda: hga.hga_paged_decode(qd, kp, vp, table, lens, window=5, sinks=-2),
+        lambda: hga.hga_paged_decode(qd, kp, vp, table, lens, scale=-1.0),
+        lambda: hga.hga_paged_decode(qd, kp, vp, table, lens, out=qd.float()),
+        lambda: hga.hga_paged_decode(qd, kp, vp, table, lens, workspace=torch.empty(64, device="cuda")),
+        lambda: hga.hga_paged_decode(qd[:0], kp, vp, table[:0], lens[:0]),
+        lambda: hga.hga_paged_plan(lens, lens, slot, i32([0]), table, 3, 4),
+        lambda: hga.hga_paged_plan(lens, lens, slot, i32([0]), table, 16, -1),
+        lambda: hga.hga_paged_plan(lens, lens.long(), slot, i32([0]), table, 16, 4),
+        lambda: hga.hga_paged_plan(lens[:1], lens, slot, i32([0]), table, 16, 4),
+        lambda: hga.hga_paged_plan(lens, lens, slot, i32([0]), table, 16, 4, slot=slot),
+        lambda: hga.hga_paged_plan(lens, lens, slot, i32([0, 0]), table, 16, 4),
+        lambda: hga.hga_paged_plan(lens, lens, slot, i32([0]), table[0], 16, 4),
+    ]
+    before = x.clone()
+    for i, call in enumerate(cases):
+        with pytest.raises(hga.HGAError):
+            call()
+            pytest.fail(f"case {i} was not refused")
+    torch.cuda.synchronize()
+    assert torch.equal(before, x) and hga.hga_device_status() == 0
 
 
 # ------------------------------------------------------ a run of them all --
