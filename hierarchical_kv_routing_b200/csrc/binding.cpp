@@ -9,14 +9,17 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/LegacyTypeDispatch.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <numeric>
 #include <sstream>
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "../../include/hga.h"
 
@@ -282,14 +285,18 @@ PyObject *plan(PyObject *const *a) {
     int32_t **const at_[6] = {&io.lens_out, &io.free_count_out, &io.cu_tokens,
                               &io.granted,  &io.slot,           &io.pos};
     // one allocation for what the caller does not bring
-    at::Tensor out[6], all;
-    int64_t total = 0, used = 0;
-    for (int i = 0; i < 6; ++i) total += none(a[8 + i]) ? size[i] : 0;
-    if (total) all = c.empty({total}, at::kInt);
+    at::Tensor out[6];
+    std::vector<int64_t> missing;
+    for (int i = 0; i < 6; ++i)
+        if (none(a[8 + i])) missing.push_back(size[i]);
+    std::vector<at::Tensor> parts;
+    if (!missing.empty())
+        parts = c.empty({std::accumulate(missing.begin(), missing.end(), (int64_t)0)}, at::kInt)
+                    .split_with_sizes(missing);
+    size_t used = 0;
     for (int i = 0; i < 6; ++i) {
         if (none(a[8 + i])) {
-            out[i] = all.defined() ? all.narrow(0, used, size[i]) : c.empty({0}, at::kInt);
-            used += size[i];
+            out[i] = std::move(parts[used++]);
             *at_[i] = out[i].data_ptr<int32_t>();
         } else {
             *at_[i] = ints(a[8 + i], name[i], {size[i]}, c);
@@ -458,6 +465,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
         return nullptr;
     }
     try {
+        // new tensors and views of them take no part in automatic differentiation
+        const at::AutoDispatchBelowADInplaceOrView below;
         return F(args);
     } catch (const Refused &e) {
         PyErr_SetString(g_error ? g_error : PyExc_RuntimeError, e.what());

@@ -30,7 +30,6 @@
 // from the block table one tile ahead of its loads.  The warps of a KV head take
 // its tiles in turn and are merged in shared memory at an item's end.
 #include <algorithm>
-#include <climits>
 
 #include "paged_internal.cuh"
 #include "sm100.cuh"
@@ -120,9 +119,9 @@ __device__ __forceinline__ int units_of(int n, int uk) { return n / uk + (n % uk
 // A CTA's walk over its units: the segment [k0, k1) of item (b, it) that is next.
 struct Walk {
     int b, it, u, nu, cnt;
-    long long left;
+    int left;
     Visible v;
-    __device__ __forceinline__ void take() { cnt = (int)min((long long)(nu - u), left); }
+    __device__ __forceinline__ void take() { cnt = min(nu - u, left); }
     __device__ __forceinline__ int k0(int uk) const { return u * uk; }
     __device__ __forceinline__ int k1(int uk) const {
         return u + cnt >= nu ? v.n : (u + cnt) * uk;
@@ -470,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     constexpr int kKeys = Tile::kKeys, kCpr = D * (int)sizeof(T) / 16, kLoads = kTileBytes / 512;
     extern __shared__ __align__(1024) char ring[];
     __shared__ int start[6];       // of the CTA's first unit: b, item, unit; the row's Visible
-    __shared__ long long sums[kWarps];
+    __shared__ int sums[kWarps];
     __shared__ uint32_t valid[kWarps][kStages];
     __shared__ float2 ml[kWarps][Tile::kMerge];
     __shared__ __align__(16) float ps[sizeof(T) == 4 ? kWarps * kRows * kKeys * 2 : 1];
@@ -487,21 +486,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     // ---- where this CTA's units begin: sums over runs of sequences, one per thread
     const int per = (A.B + kThreads - 1) / kThreads;
     const int r0 = min(A.B, tid * per), r1 = min(A.B, r0 + per);
-    long long mine = 0;
+    int mine = 0;
     Visible v = {0, 0, 0};
     for (int b = r0; b < r1; ++b) {
         v = visible(A, b);
-        mine += (long long)units_of(v.n, uk) * S.items;
+        mine += units_of(v.n, uk) * S.items;
     }
-    long long upto = mine;
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
     }
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    long long before = upto - mine, U = 0;
+    int before = upto - mine, U = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += sums[w];
@@ -509,31 +508,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     }
     // with fewer units than CTAs the last ones take none, so that a split item's
     // parts lie in CTAs without a gap
-    const int n = U < S.n ? (int)U : S.n;
-    long long u0 = 0, u1 = 0;
-    if (range < n) {
-        // floor(U i / n) = U / n i + (U mod n) i / n, with a 64-bit division only where
-        // the line is that long
-        const bool small = U <= INT_MAX;
-        const long long each = small ? (unsigned)U / (unsigned)n : U / n;
-        const unsigned rest = (unsigned)(U - each * n);
-        u0 = each * range + rest * (unsigned)range / (unsigned)n;
-        u1 = each * (range + 1) + rest * (unsigned)(range + 1) / (unsigned)n;
-    }
+    const int n = min(U, S.n);
+    // floor(U i / n) = U / n i + (U mod n) i / n, whose products fit 32 bits
+    const int each = n ? U / n : 0, rest = n ? U - each * n : 0;
+    auto begin_of = [&](int i) { return each * i + rest * i / n; };
+    const int u0 = range < n ? begin_of(range) : 0, u1 = range < n ? begin_of(range + 1) : 0;
     if (u0 < u1 && u0 >= before && u0 < before + mine) {
-        long long at = u0 - before;
+        int at = u0 - before;
         for (int b = r0; b < r1; ++b) {
             if (per > 1) v = visible(A, b);
             const int nu = units_of(v.n, uk);
-            if (at < (long long)nu * S.items) {
+            if (at < nu * S.items) {
                 start[0] = b;
-                const int it = at <= INT_MAX ? (int)((unsigned)at / (unsigned)nu) : (int)(at / nu);
-                start[1] = it;
-                start[2] = (int)(at - (long long)it * nu);
+                start[1] = at / nu;
+                start[2] = at % nu;
                 start[3] = v.s, start[4] = v.lo, start[5] = v.n;
                 break;
             }
-            at -= (long long)nu * S.items;
+            at -= nu * S.items;
         }
     }
     __syncthreads();
@@ -603,11 +595,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
+    // while the first tiles are on their way
+    empty_rows<T, D>(A, S);
+
     // ---- consumer
     Tile t;
     int stage = 0;
     int4 joined = make_int4(0, 0, -1, -1);
-    long long done = 0;                             // units before the segment
+    int done = 0;                                   // units before the segment
     for (;;) {
         const int k1 = C.k1(uk), h0 = C.it * kHw;
         t.begin(A, C.b, (h0 + hsub) * A.G + g0, heads);
@@ -664,9 +659,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
         }
         if (!cont) {
             if (open) {
-                // the range that holds the item's last unit
-                const long long last = u0 + done + C.nu - 1;
-                joined = make_int4(C.b, C.it, range, (int)(((last + 1) * n - 1) / U));
+                // the range that holds the item's last unit: a guess, put right
+                const int last = u0 + done + C.nu - 1;
+                int r = min(n - 1, (int)((float)last * (float)n / (float)U));
+                while (begin_of(r) > last) --r;
+                while (r + 1 < n && begin_of(r + 1) <= last) ++r;
+                joined = make_int4(C.b, C.it, range, r);
             }
             if (S.by_item && tid == 0)
                 S.join[((int64_t)C.b * S.items + C.it) * S.gsplit + chunk] = joined;
@@ -676,7 +674,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     }
     if (!S.by_item && tid == 0) S.join[cta] = joined;
     asm volatile("cp.async.wait_all;" ::: "memory");
-    empty_rows<T, D>(A, S);
 }
 
 // Adds up the parts of the items that were split, in CTA order; a programmatic
@@ -860,6 +857,7 @@ hga_status launch_paged_decode(const PagedArgs &A, int dtype, int D, void *ws, c
     if (A.window > 0) most = std::min(most, (long long)A.window + A.sinks);
     const int uk = kUnitTiles * (kTileBytes / (D * (dtype == HGA_BF16 ? 2 : 4)));
     const long long units = (most + uk - 1) / uk * S.items * A.B;
+    if (units > 0x7fffffffLL) return HGA_ERR_UNSUPPORTED;       // the kernel counts them in 32 bits
     S.n = (int)std::max(1ll, std::min(units, (long long)std::min(2 * sm_count(), kMaxCtas) / S.gsplit));
     if (dtype == HGA_BF16) {
         if (D == 128)

@@ -356,7 +356,9 @@ hga_status hga_hostkv_plan_for(const hga_dims *dims, const hga_params *prm,
  * on the host, so a serving step can be captured in a CUDA graph.
  *
  * Limits: page_size a power of two; num_pages * page_size, max_pages *
- * page_size and B * max_pages below 2^31; B and Hkv at most 65535; D 64 or 128.
+ * page_size and B * max_pages below 2^31; B and Hq at most 65535; D 64 or 128;
+ * for hga_paged_decode also B * Hkv * max_pages * page_size (max_pages * page_size
+ * at most window + sinks with a window) below 2^36.
  * int32 buffers need 4-byte alignment, rows of q, k, v, pages and gradients
  * 16-byte alignment.  Outputs must not overlap inputs except where stated. */
 typedef struct hga_paged_dims {

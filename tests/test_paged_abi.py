@@ -127,6 +127,8 @@ def test_decode_pointers_values_and_workspace(lib):
     for kw in (dict(window=-1), dict(sinks=-1), dict(scale=-1.0), dict(scale=float("nan")),
                dict(scale=float("inf"))):
         assert decode_call(lib, pdims(), **kw) == INVALID
+    # more units of work than 32 bits count
+    assert decode_call(lib, pdims(B=1024, max_pages=1 << 20, page_size=1024)) == UNSUPPORTED
     need = lib.hga_paged_decode_workspace(ctypes.byref(pdims()))
     assert need > 0
     assert decode_call(lib, pdims(), nbytes=need - 1) == WORKSPACE
