@@ -717,6 +717,71 @@ def test_binding_refusals(hga):
     assert torch.equal(before, x) and hga.hga_device_status() == 0
 
 
+def test_captured_gradient_follows_its_inputs(hga):
+    """The gradient in two CUDA graphs on one workspace: replays follow the inputs, in a
+    batched [B, T] layout with an odd head count."""
+    N, Hq, Hkv, D = 22, 5, 1, 64
+    rope = hga.HGARope(rotary_dim=32, layout="interleaved", theta=1e4)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    w = weights(3, D, "bf16")
+    x, q, k, v = qkv(1, N, Hq, Hkv, D, "bf16")
+    d = [torch.randn(2, N // 2, h, D, device="cuda") for h in (Hq, Hkv, Hkv)]
+    pos = i32(np.arange(N).reshape(2, -1))
+
+    def call(ws=None):
+        return hga.hga_qk_norm_rope_backward(q.unflatten(0, (2, -1)), k.unflatten(0, (2, -1)), d[0], d[1],
+                                             pos, rope, q_weight=w[0], k_weight=w[1], d_v=d[2],
+                                             workspace=ws)
+    call(ws)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call(ws)
+        graphs.append((g, out))
+    for i in range(4):
+        x.copy_(qkv(50 + i, N, Hq, Hkv, D, "bf16")[0])
+        d[0].normal_(), pos.add_(i)
+        want = call()
+        g, got = graphs[i % 2]
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_first_calls_in_a_capture(hga):
+    """A process whose first call of every operator is captured: the graph replays."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, hierarchical_kv_routing_b200 as hga
+z = lambda *s, **k: torch.zeros(*s, device="cuda", **k)
+i = lambda *s: z(*s, dtype=torch.int32)
+c = hga.PagedKVCache(2, 8, 4, 4, 2, 64, torch.bfloat16)
+new, x, w = i(2) + 1, torch.randn(2, 8, 64, device="cuda").bfloat16(), z(64).bfloat16() + 1
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    p = hga.hga_paged_plan(c.lens, new, c.free_pages, c.free_count, c.block_table, 4, 2,
+                           lens_out=c.lens, free_count_out=c.free_count)
+    q, _, _ = hga.hga_qk_norm_rope(x[:, :4], x[:, 4:6], x[:, 6:], p["pos"], hga.HGARope(), q_weight=w,
+                                   k_weight=w, k_pages=c.k_pages, v_pages=c.v_pages, slot=p["slot"])
+    out = hga.hga_paged_decode(q, c.k_pages, c.v_pages, c.block_table, c.lens)
+    grads = hga.hga_qk_norm_rope_backward(x[:, :4], x[:, 4:6], q, q[:, :2].contiguous(), p["pos"],
+                                          hga.HGARope(), q_weight=w, k_weight=w)
+g.replay()
+torch.cuda.synchronize()
+assert c.lens.tolist() == [1, 1] and torch.equal(out[:, :2], x[:, 6:7].expand(2, 2, 64))
+assert all(t is None or t.isfinite().all() for t in grads) and hga.hga_device_status() == 0
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
 # ------------------------------------------------------ a run of them all --
 
 @pytest.mark.parametrize("dtype,layout", [("bf16", "half"), ("f32", "interleaved")])
