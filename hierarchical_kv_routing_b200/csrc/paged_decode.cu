@@ -680,8 +680,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
 // dependent of k_paged_decode.  grid: (possible split items, rows).  Latency
 // bound: an item of up to kFew parts is joined by its first CTA, a group of D / 4
 // lanes per row and four parts loaded at a time; beyond that every row has its
-// CTA, whose groups share the parts.  (One CTA per row throughout: 12 us instead
-// of 4 for 384 items of 2 or 3 parts.)
+// CTA, whose groups share the parts.  (Whole calls: 96 rows of 640 keys, 384 items of
+// 2 or 3 parts, 23 us, 31 with a CTA per row; 1 x 32K, 4 items of 74 parts, 15 us, 28
+// with a CTA per item.)
 constexpr int kJoinThreads = 256, kAhead = 8, kFew = 16;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs A, const Split S) {

@@ -834,9 +834,11 @@ void set_work(QkWork &K, int N, int64_t tokens) {
         K.steps[i] = K.full[i] + (K.rest[i] > 0);
         steps += K.steps[i];
     }
-    // a warp per token where that fills the card; fewer tokens are spread over more
-    // warps (each forms the angles again), down to one step a warp
-    const int64_t want = 148 * 16;
+    // Few tokens are spread over several warps each, up to four warps per SM and down
+    // to one step a warp; every warp forms the angles again.  32 + 4 + 4 heads of 128,
+    // forward: 16 tokens 3.8 us (a warp per token: 6.2), 256 4.9 (6.4), 1024 6.5; with
+    // up to sixteen warps per SM 256 5.7, 1024 9.0.
+    const int64_t want = 148 * 4;
     K.split = tokens == 0 ? 1 : (int)std::min<int64_t>(std::max(steps, 1), std::max<int64_t>(1, (want + tokens - 1) / tokens));
     K.warps = (unsigned)(tokens * K.split);
 }

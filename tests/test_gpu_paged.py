@@ -76,7 +76,7 @@ def test_plan_steps(hga, B, page, M, top, pad):
     assert hga.hga_device_status() == 0
 
 
-@pytest.mark.parametrize("n", [8191, 8192, 8193, 70001])
+@pytest.mark.parametrize("n", [2047, 2048, 2049, 8192, 70001])
 def test_plan_prompts_in_both_fills(hga, n):
     """Prompts whose tokens the scanning CTA fills itself, and beyond."""
     rng = np.random.default_rng(n)
