@@ -148,38 +148,38 @@ struct Walk {
 // accumulator, exponentiated and rounded, is the A operand of O += P V, V read
 // transposed.  Rows of shared memory are XOR-swizzled in 16-byte chunks so the
 // eight rows of an ldmatrix fall in different banks.  kRows = 8 leaves the upper
-// half of the tile out of everything but the products.
+// half of the tile out of everything but the products; kRows = 32 is two tiles that
+// share every fragment of K and V.
 template <int D, int kRows> struct TileBf16 {
     using T = __nv_bfloat16;
     static constexpr int kKeys = kTileBytes / (D * 2), kSwz = 7, kMerge = 8;
-    static constexpr int R = kRows / 8;
-    uint32_t q[D / 16][4];
-    float o[D / 8][4];
-    float m[R], l[R];
+    static constexpr int M = kRows > 16 ? kRows / 16 : 1;   // tiles
+    static constexpr int R = kRows > 8 ? 2 : 1;             // row groups of a tile in use
+    uint32_t q[M][D / 16][4];
+    float o[M][D / 8][4];
+    float m[M][R], l[M][R];
 
     __device__ __forceinline__ void begin(const PagedArgs &A, int b, int head0, int heads) {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = (lane & 3) * 2;
         const T *base = static_cast<const T *>(A.q) + ((int64_t)b * A.Hq + head0) * D + c;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
+        for (int t = 0; t < M; ++t) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) q[i][j] = 0;
-            const T *p = base + i * 16;
-            if (g < heads) {
-                q[i][0] = *reinterpret_cast<const uint32_t *>(p + g * D);
-                q[i][2] = *reinterpret_cast<const uint32_t *>(p + g * D + 8);
-            }
-            if (R == 2 && g + 8 < heads) {
-                q[i][1] = *reinterpret_cast<const uint32_t *>(p + (g + 8) * D);
-                q[i][3] = *reinterpret_cast<const uint32_t *>(p + (g + 8) * D + 8);
-            }
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = t * 16 + g + (j & 1) * 8;
+                    q[t][i][j] = 0;
+                    if ((j & 1) < R && row < heads)
+                        q[t][i][j] = *reinterpret_cast<const uint32_t *>(base + row * D + i * 16 + (j >> 1) * 8);
+                }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) m[t][r] = -INFINITY, l[t][r] = 0.f;
         }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) m[r] = -INFINITY, l[r] = 0.f;
     }
 
     // valid: bit k set if key k of the tile counts
@@ -187,11 +187,13 @@ template <int D, int kRows> struct TileBf16 {
                                          float *) {
         constexpr int NT = kKeys / 8;
         const int lane = threadIdx.x & 31, c = (lane & 3) * 2;
-        float s[NT][4];
+        float s[M][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int t = 0; t < M; ++t)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[n][j] = 0.f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[t][n][j] = 0.f;
         // matrices of an x4 load: keys 0-7 and 8-15 of the pair, two chunks of 8 dimensions
         const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
 #pragma unroll
@@ -200,94 +202,115 @@ template <int D, int kRows> struct TileBf16 {
             for (int n = 0; n < NT; n += 2) {
                 uint32_t f[4];
                 ldsm4(f, ks + (n * 8 + krow) * (D * 2) + (((i * 2 + kch) ^ (lane & 7)) << 4));
-                mma16816(s[n], q[i], f[0], f[1]);
-                mma16816(s[n + 1], q[i], f[2], f[3]);
+#pragma unroll
+                for (int t = 0; t < M; ++t) {
+                    mma16816(s[t][n], q[t][i], f[0], f[1]);
+                    mma16816(s[t][n + 1], q[t][i], f[2], f[3]);
+                }
             }
-        float top[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) top[r] = -INFINITY;
-        constexpr uint32_t full = kKeys == 32 ? 0xffffffffu : (1u << kKeys) - 1u;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 2 * R; ++j) {
-                s[n][j] *= scale;
-                if (valid != full && !((valid >> (n * 8 + c + (j & 1))) & 1u)) s[n][j] = -INFINITY;
-                top[j >> 1] = fmaxf(top[j >> 1], s[n][j]);
-            }
+        constexpr uint32_t full = kKeys == 32 ? 0xffffffffu : (1u << (kKeys & 31)) - 1u;
+        float top[M][R];
         bool grow = false;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-            // the reference moves only when the maximum passes it by 2^8: weights and
-            // sums stay far from fp32's range, and O is rarely rescaled
-            grow |= top[r] > m[r] + 8.f;
+        for (int t = 0; t < M; ++t) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) top[t][r] = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2 * R; ++j) {
+                    float &x = s[t][n][j];
+                    x *= scale;
+                    if (valid != full && !((valid >> (n * 8 + c + (j & 1))) & 1u)) x = -INFINITY;
+                    top[t][j >> 1] = fmaxf(top[t][j >> 1], x);
+                }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                top[t][r] = fmaxf(top[t][r], __shfl_xor_sync(0xffffffffu, top[t][r], 1));
+                top[t][r] = fmaxf(top[t][r], __shfl_xor_sync(0xffffffffu, top[t][r], 2));
+                // the reference moves only when the maximum passes it by 2^8: weights and
+                // sums stay far from fp32's range, and O is rarely rescaled
+                grow |= top[t][r] > m[t][r] + 8.f;
+            }
         }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float nm = top[r] > m[r] + 8.f ? top[r] : m[r];
-                const float f = nm == -INFINITY ? 1.f : ex2(m[r] - nm);
-                m[r] = nm;
-                l[r] *= f;
+            for (int t = 0; t < M; ++t)
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    o[i][2 * r] *= f;
-                    o[i][2 * r + 1] *= f;
+                for (int r = 0; r < R; ++r) {
+                    const float nm = top[t][r] > m[t][r] + 8.f ? top[t][r] : m[t][r];
+                    const float f = nm == -INFINITY ? 1.f : ex2(m[t][r] - nm);
+                    m[t][r] = nm;
+                    l[t][r] *= f;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        o[t][i][2 * r] *= f;
+                        o[t][i][2 * r + 1] *= f;
+                    }
                 }
-            }
         }
-        float ref[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) ref[r] = m[r] == -INFINITY ? 0.f : m[r];
+        for (int t = 0; t < M; ++t) {
+            float ref[R];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+            for (int r = 0; r < R; ++r) ref[r] = m[t][r] == -INFINITY ? 0.f : m[t][r];
 #pragma unroll
-            for (int j = 0; j < 2 * R; ++j) {
-                s[n][j] = ex2(s[n][j] - ref[j >> 1]);
-                l[j >> 1] += s[n][j];
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 2 * R; ++j) {
+                    s[t][n][j] = ex2(s[t][n][j] - ref[j >> 1]);
+                    l[t][j >> 1] += s[t][n][j];
+                }
+        }
         const int vrow = lane & 15, vch = lane >> 4;
 #pragma unroll
         for (int kb = 0; kb < kKeys / 16; ++kb) {
             // the weights are rounded to bf16 (at most half a step, 2^-8 relative) for the product;
             // their sum above is of the unrounded ones
-            uint32_t p[4] = {pack2(s[2 * kb][0], s[2 * kb][1]), 0u,
-                             pack2(s[2 * kb + 1][0], s[2 * kb + 1][1]), 0u};
-            if (R == 2) {
-                p[1] = pack2(s[2 * kb][2], s[2 * kb][3]);
-                p[3] = pack2(s[2 * kb + 1][2], s[2 * kb + 1][3]);
-            }
+            uint32_t p[M][4];
+#pragma unroll
+            for (int t = 0; t < M; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float *x = s[t][2 * kb + (j >> 1)] + (j & 1) * 2;
+                    p[t][j] = (j & 1) < R ? pack2(x[0], x[1]) : 0u;
+                }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 uint32_t f[4];
                 ldsm4_t(f, vs + (kb * 16 + vrow) * (D * 2) + (((i * 2 + vch) ^ (lane & 7)) << 4));
-                mma16816(o[2 * i], p, f[0], f[1]);
-                mma16816(o[2 * i + 1], p, f[2], f[3]);
+#pragma unroll
+                for (int t = 0; t < M; ++t) {
+                    mma16816(o[t][2 * i], p[t], f[0], f[1]);
+                    mma16816(o[t][2 * i + 1], p[t], f[2], f[3]);
+                }
             }
         }
     }
 
     __device__ __forceinline__ void end() {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        }
+        for (int t = 0; t < M; ++t)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 1);
+                l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 2);
+            }
     }
     // rows round * kMerge .. + kMerge of this warp
     __device__ __forceinline__ void put(int round, float *rows, float2 *ml) const {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = (lane & 3) * 2;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (r == round) {
+        for (int t = 0; t < M; ++t)
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    *reinterpret_cast<float2 *>(rows + g * D + i * 8 + c) =
-                        make_float2(o[i][2 * r], o[i][2 * r + 1]);
-                if ((lane & 3) == 0) ml[g] = make_float2(m[r], l[r]);
-            }
+            for (int r = 0; r < R; ++r)
+                if (t * 2 + r == round) {
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i)
+                        *reinterpret_cast<float2 *>(rows + g * D + i * 8 + c) =
+                            make_float2(o[t][i][2 * r], o[t][i][2 * r + 1]);
+                    if ((lane & 3) == 0) ml[g] = make_float2(m[t][r], l[t][r]);
+                }
     }
 };
 
@@ -802,14 +825,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs A, 
 
 Split make_split(int B, int Hq, int Hkv, int D, int dtype) {
     Split S = {};
-    const int G = Hq / Hkv, most = dtype == HGA_BF16 ? 16 : 8;
+    const int G = Hq / Hkv, most = dtype == HGA_F32 ? 8 : D == 64 ? 32 : 16;
     // Runs of 256 bytes: bf16 heads of 64 are taken in pairs (64 x 16K tokens of 8
     // heads: 366 us one by one, 320 in pairs); for rows of 256 bytes and more one head
     // a CTA is faster, as four times the parts cost more than longer runs give (16 x
     // 64K tokens of 4 heads of 128: 316 us against 326 for four heads).
     S.hw = D * (dtype == HGA_BF16 ? 2 : 4) < 256 && Hkv % 2 == 0 ? 2 : 1;
-    // More query heads than a tile has rows are cut into chunks; the CTAs of a range's
-    // chunks run side by side, so that the second reads K and V from L2.
+    // More query heads than registers hold rows for (bf16 heads of 64: 32, of 128: 16;
+    // fp32: 8) are cut into chunks; the CTAs of a range's chunks run side by side, so
+    // that the second reads K and V from L2.
     S.gsplit = (G + most - 1) / most;
     S.gch = (G + S.gsplit - 1) / S.gsplit;
     S.gsplit = (G + S.gch - 1) / S.gch;
@@ -865,10 +889,12 @@ hga_status launch_paged_decode(const PagedArgs &A, int dtype, int D, void *ws, c
             return S.gch > 8 ? run<TileBf16<128, 16>, 128, 16, 1>(A, S, st)
                              : run<TileBf16<128, 8>, 128, 8, 1>(A, S, st);
         if (S.hw == 2)
-            return S.gch > 8 ? run<TileBf16<64, 16>, 64, 16, 2>(A, S, st)
-                             : run<TileBf16<64, 8>, 64, 8, 2>(A, S, st);
-        return S.gch > 8 ? run<TileBf16<64, 16>, 64, 16, 1>(A, S, st)
-                         : run<TileBf16<64, 8>, 64, 8, 1>(A, S, st);
+            return S.gch > 16  ? run<TileBf16<64, 32>, 64, 32, 2>(A, S, st)
+                   : S.gch > 8 ? run<TileBf16<64, 16>, 64, 16, 2>(A, S, st)
+                               : run<TileBf16<64, 8>, 64, 8, 2>(A, S, st);
+        return S.gch > 16  ? run<TileBf16<64, 32>, 64, 32, 1>(A, S, st)
+               : S.gch > 8 ? run<TileBf16<64, 16>, 64, 16, 1>(A, S, st)
+                           : run<TileBf16<64, 8>, 64, 8, 1>(A, S, st);
     }
     if (D == 128)
         return S.gch > 4 ? run<TileF32<128, 8>, 128, 8, 1>(A, S, st)

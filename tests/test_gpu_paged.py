@@ -391,7 +391,7 @@ def check_decode(hga, q, kp, vp, table, lens, dtype, window=0, sinks=0, scale=0.
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("Hq,Hkv,D", [(1, 1, 64), (4, 4, 128), (8, 8, 64), (32, 4, 128), (6, 2, 64),
                                       (5, 1, 128), (9, 1, 64), (16, 1, 128), (20, 1, 64), (34, 2, 128),
-                                      (40, 4, 64), (7, 7, 128)])
+                                      (40, 4, 64), (7, 7, 128), (50, 2, 64), (64, 2, 64), (33, 1, 64)])
 @pytest.mark.parametrize("page", [16, 64])
 def test_decode_heads_and_lengths(hga, dtype, Hq, Hkv, D, page):
     """Lengths of nothing, one token, and both sides of pages, tiles and units."""
