@@ -398,7 +398,9 @@ typedef struct hga_paged_plan_io {
  * never refused for want of pages.  Packed token t of sequence b
  * (cu_tokens[b] <= t < cu_tokens[b+1]) has position lens + t - cu_tokens[b];
  * entries from cu_tokens[B] to n_slots get slot -1 and position 0, so a step of
- * fewer tokens can replay a graph of n_slots.  Of dims, B, num_pages, page_size
+ * fewer tokens can replay a graph of n_slots.  Pages are not counted: a page that
+ * several rows hold (a shared prefix may be read so) must not be given back by more
+ * than one of them, nor be one that a row still writes to.  Of dims, B, num_pages, page_size
  * and max_pages are read.
  * A negative length or count, a length beyond the row, a stack size outside
  * [0, num_pages], a page id outside [0, num_pages) and a release that would

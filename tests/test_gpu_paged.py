@@ -645,6 +645,21 @@ def test_allocations_of_another_stream_do_not_wait_for_this_one(hga):
         assert all(torch.equal(a, b) for a, b in zip(got, ref_out))
 
 
+def test_results_are_ordinary_tensors(hga):
+    """What comes back can be changed in place and differentiated through."""
+    _, q, k, v = qkv(1, 6, 4, 2, 64, "f32")
+    o = list(hga.hga_qk_norm_rope(q, k, v, i32(np.arange(6)), hga.HGARope()))
+    p = hga.hga_paged_plan(i32([1, 2]), i32([1, 1]), i32([2, 3]), i32([2]), i32([[0, 0], [1, 0]]), 4, 4)
+    before = {n: t.clone() for n, t in p.items()}
+    p["slot"].add_(5)
+    assert all(torch.equal(p[n], before[n] + (5 if n == "slot" else 0)) for n in p)
+    for t in o:
+        assert not t.is_inference() and not t.requires_grad
+        t.mul_(2.0).requires_grad_()
+    sum((t * t).sum() for t in o).backward()
+    assert all(torch.equal(t.grad, 2 * t) for t in o)
+
+
 def test_binding_refusals(hga):
     """Tensors of the wrong kind are refused with a message before anything runs."""
     rope = hga.HGARope()
@@ -678,6 +693,7 @@ def test_binding_refusals(hga):
         lambda: hga.hga_qk_norm_rope(q, k, v, pos, rope._replace(rotary_dim=24)),
         lambda: hga.hga_qk_norm_rope(q, k, v, pos, "half"),
         lambda: hga.hga_qk_norm_rope(q.unflatten(0, (2, 3)), k, v, pos, rope),
+        lambda: hga.hga_qk_norm_rope(x[:, 4:260].unflatten(-1, (4, 64)), k, v, pos, rope),  # 8 bytes off
         lambda: hga.hga_qk_norm_rope_backward(q, k, d[0].half(), d[1].half(), pos, rope),
         lambda: hga.hga_qk_norm_rope_backward(q, k, d[0], d[1].bfloat16(), pos, rope),
         lambda: hga.hga_qk_norm_rope_backward(q, k, d[0], d[1], pos, rope, dv=d[2]),
