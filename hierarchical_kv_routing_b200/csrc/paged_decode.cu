@@ -101,6 +101,10 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Where chunk c (16 bytes) of merge row r lies in its row: the four rows that a
+// half-warp's 8-byte stores touch fall in different banks.
+__device__ __forceinline__ int merge_chunk(int c, int r) { return c ^ (2 * r); }
+
 // The visible tokens of a row: s first ones, then lo .. ; n in all.
 struct Visible {
     int s, lo, n;
@@ -307,7 +311,8 @@ template <int D, int kRows> struct TileBf16 {
                 if (t * 2 + r == round) {
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i)
-                        *reinterpret_cast<float2 *>(rows + g * D + i * 8 + c) =
+                        *reinterpret_cast<float2 *>(rows + g * D + merge_chunk(i * 2 + (c >> 2), g) * 4 +
+                                                    (c & 2)) =
                             make_float2(o[t][i][2 * r], o[t][i][2 * r + 1]);
                     if ((lane & 3) == 0) ml[g] = make_float2(m[t][r], l[t][r]);
                 }
@@ -448,7 +453,8 @@ template <int D, int kRows> struct TileF32 {
 #pragma unroll
         for (int r = 0; r < kRows; ++r)
             if (r / kMerge == round && lane < LPR)
-                *reinterpret_cast<ulonglong2 *>(rows + (r % kMerge) * D + lane * 4) =
+                *reinterpret_cast<ulonglong2 *>(rows + (r % kMerge) * D +
+                                                merge_chunk(lane, r % kMerge) * 4) =
                     make_ulonglong2(o[r][0], o[r][1]);
         if (lane < kRows && lane / kMerge == round) ml[lane % kMerge] = make_float2(m, l);
     }
@@ -626,9 +632,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     int stage = 0;
     int4 joined = make_int4(0, 0, -1, -1);
     int done = 0;                                   // units before the segment
-    for (;;) {
-        const int k1 = C.k1(uk), h0 = C.it * kHw;
-        t.begin(A, C.b, (h0 + hsub) * A.G + g0, heads);
+    t.begin(A, C.b, (C.it * kHw + hsub) * A.G + g0, heads);
+    for (bool more = true; more;) {
+        const int k1 = C.k1(uk), h0 = C.it * kHw, b = C.b;
         for (int k = C.k0(uk) + ksub * kKeys; k < k1; k += kKeys * kKw) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
             __syncwarp();
@@ -642,16 +648,35 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
         // ---- the segment's rows: merged over the warps, then out or parked
         const bool cont = C.u > 0, open = C.u + C.cnt < C.nu, whole = !cont && !open;
         const int64_t row_at = ((int64_t)cta * 2 + (cont ? 0 : 1)) * S.rows;
+        if (!cont) {
+            if (open) {
+                // the range that holds the item's last unit: a guess, put right
+                const int last = u0 + done + C.nu - 1;
+                int r = min(n - 1, (int)((float)last * (float)n / (float)U));
+                while (begin_of(r) > last) --r;
+                while (r + 1 < n && begin_of(r + 1) <= last) ++r;
+                joined = make_int4(b, C.it, range, r);
+            }
+            if (S.by_item && tid == 0)
+                S.join[((int64_t)b * S.items + C.it) * S.gsplit + chunk] = joined;
+        }
+        done += C.cnt;
+        constexpr int kRounds = (kRows + Tile::kMerge - 1) / Tile::kMerge;
 #pragma unroll
-        for (int round = 0; round < (kRows + Tile::kMerge - 1) / Tile::kMerge; ++round) {
+        for (int round = 0; round < kRounds; ++round) {
             t.put(round, merge + warp * Tile::kMerge * D, ml[warp]);
+            if (round == kRounds - 1) {
+                // the next segment's queries come while this one's rows are merged
+                more = C.next(A, S, uk);
+                if (more) t.begin(A, C.b, (C.it * kHw + hsub) * A.G + g0, heads);
+            }
             __syncthreads();
             for (int e = tid; e < kHw * Tile::kMerge * (D / 4); e += kThreads) {
-                const int d = (e % (D / 4)) * 4, r = e / (D / 4) % Tile::kMerge;
+                const int ch = e % (D / 4), d = ch * 4, r = e / (D / 4) % Tile::kMerge;
                 const int hs = e / (D / 4 * Tile::kMerge), row = round * Tile::kMerge + r;
                 if (row >= heads) continue;
                 float top = -INFINITY;
-                #pragma unroll
+#pragma unroll
                 for (int k = 0; k < kKw; ++k) top = fmaxf(top, ml[k * kHw + hs][r].x);
                 const float ref = top == -INFINITY ? 0.f : top;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -660,15 +685,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
                 for (int k = 0; k < kKw; ++k) {
                     const int w = k * kHw + hs;
                     const float f = ex2(ml[w][r].x - ref);
-                    const float4 x =
-                        *reinterpret_cast<const float4 *>(merge + (w * Tile::kMerge + r) * D + d);
+                    const float4 x = *reinterpret_cast<const float4 *>(
+                        merge + (w * Tile::kMerge + r) * D + merge_chunk(ch, r) * 4);
                     sum = fmaf(ml[w][r].y, f, sum);
                     a.x = fmaf(x.x, f, a.x), a.y = fmaf(x.y, f, a.y);
                     a.z = fmaf(x.z, f, a.z), a.w = fmaf(x.w, f, a.w);
                 }
                 if (whole) {
                     const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-                    const int64_t at = (int64_t)C.b * A.Hq + (h0 + hs) * A.G + g0 + row;
+                    const int64_t at = (int64_t)b * A.Hq + (h0 + hs) * A.G + g0 + row;
                     put4<T>(static_cast<T *>(A.out) + at * D + d,
                             make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
                     if (A.lse && d == 0) A.lse[at] = (top + log2f(sum)) * kLn2;
@@ -680,20 +705,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
             }
             __syncthreads();
         }
-        if (!cont) {
-            if (open) {
-                // the range that holds the item's last unit: a guess, put right
-                const int last = u0 + done + C.nu - 1;
-                int r = min(n - 1, (int)((float)last * (float)n / (float)U));
-                while (begin_of(r) > last) --r;
-                while (r + 1 < n && begin_of(r + 1) <= last) ++r;
-                joined = make_int4(C.b, C.it, range, r);
-            }
-            if (S.by_item && tid == 0)
-                S.join[((int64_t)C.b * S.items + C.it) * S.gsplit + chunk] = joined;
-        }
-        done += C.cnt;
-        if (!C.next(A, S, uk)) break;
     }
     if (!S.by_item && tid == 0) S.join[cta] = joined;
     asm volatile("cp.async.wait_all;" ::: "memory");
