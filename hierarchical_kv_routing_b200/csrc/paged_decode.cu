@@ -40,6 +40,7 @@ __device__ int g_paged_error = 0;
 
 namespace {
 
+using sm100::ex2;
 using sm100::f2_fma;
 using sm100::f2_mul;
 using sm100::f2_pack;
@@ -62,9 +63,6 @@ struct Split {
     int4 *join;        // entry: (sequence, item, first range, last range); first -1: not split
 };
 
-__device__ __forceinline__ uint32_t su32(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
 // 16 bytes to shared memory; zeros, and no read, where live is false
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -90,11 +88,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -572,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     C.take();
     Walk P = C;
     char *kring = ring + warp * kStages * 2 * kTileBytes;
-    const uint32_t ring_s = su32(kring);
+    const uint32_t ring_s = sm100::smem_addr(kring);
     const int64_t row_bytes = (int64_t)A.Hkv * D * (int)sizeof(T);
     const int page_mask = (1 << A.log2_page) - 1;
 
