@@ -124,36 +124,36 @@ __global__ void __launch_bounds__(kThreads) k_plan_scan(const PlanArgs a, int fi
             ends[tid + 1] = (int)(before + give);
             if (tid == 0) ends[0] = 0;
             __syncthreads();
-            const int n = (int)total;
+            const unsigned n = (unsigned)total;    // below 2^31, but n + a step is not
             auto entry = [&](int row, int e) {
                 return a.io.block_table[(int64_t)(b0 + row) * a.max_pages + e - ends[row]];
             };
-            for (int e0 = 0; e0 < n; e0 += kThreads * kRun) {
+            for (unsigned e0 = 0; e0 < n; e0 += kThreads * kRun) {
                 // a warp takes 32 kRun entries in a row: few rows, so one search and then
                 // a look at the row's end
-                const int w0 = e0 + (tid >> 5) * 32 * kRun + (tid & 31);
-                int ids[kRun], row = find_row(ends, min(w0, n - 1));
+                const unsigned w0 = e0 + (tid >> 5) * 32 * kRun + (tid & 31);
+                int ids[kRun], row = find_row(ends, (int)min(w0, n - 1));
                 bool good = true;
 #pragma unroll
                 for (int i = 0; i < kRun; ++i) {
-                    const int e = min(w0 + i * 32, n - 1);
+                    const int e = (int)min(w0 + i * 32, n - 1);
                     if (ends[row + 1] <= e) row = find_row(ends, e);
                     ids[i] = entry(row, e);
                 }
 #pragma unroll
                 for (int i = 0; i < kRun; ++i) good &= (unsigned)ids[i] < (unsigned)a.num_pages;
-                const int many = min(n - e0, kThreads * kRun);
+                const int many = (int)min(n - e0, (unsigned)(kThreads * kRun));
                 if (__syncthreads_and(good) && stack + many <= a.num_pages) {
 #pragma unroll
                     for (int i = 0; i < kRun; ++i)
-                        if (w0 + i * 32 < n) a.io.free_pages[stack + w0 - e0 + i * 32] = ids[i];
+                        if (w0 + i * 32 < n) a.io.free_pages[stack + (w0 - e0) + i * 32] = ids[i];
                     stack += many;
                     continue;
                 }
                 // bad ids are left out, and what the stack has no room for
                 for (int i = 0; i < kRun; ++i) {
-                    const int e = e0 + i * kThreads + tid;
-                    const int id = e < n ? entry(find_row(ends, e), e) : -1;
+                    const unsigned e = e0 + i * kThreads + tid;
+                    const int id = e < n ? entry(find_row(ends, (int)e), (int)e) : -1;
                     const bool ok = (unsigned)id < (unsigned)a.num_pages;
                     long long all, at = stack + scan(ok ? 1 : 0, part, all);
                     if (ok && at < a.num_pages) a.io.free_pages[at] = id;

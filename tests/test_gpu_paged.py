@@ -173,6 +173,18 @@ def test_plan_releases_long_rows(hga, bad):
     assert hga.hga_device_status() == (5 if bads else 0)
 
 
+def test_plan_releases_a_row_of_the_largest_size(hga):
+    """One row of 2^31 - 1 pages of one token, all given back: the last sweep over its
+    entries ends beyond 31 bits."""
+    n = 2 ** 31 - 1
+    table = torch.arange(n, dtype=torch.int32, device="cuda")
+    free = torch.full((n,), -7, dtype=torch.int32, device="cuda")
+    r = hga.hga_paged_plan(i32([n]), i32([0]), free, i32([0]), table.view(1, n), 1, 1, release=i32([1]))
+    assert r["free_count"].tolist() == [n] and r["lens"].tolist() == [0]
+    assert torch.equal(free, table)
+    assert hga.hga_device_status() == 0
+
+
 # ------------------------------------------------------------- rotation --
 
 ROPES = [
