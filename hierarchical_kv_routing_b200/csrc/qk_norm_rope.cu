@@ -708,7 +708,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
             }
             // a row that does not exist is all zeros: with eps 0 its r is infinite
             const float r = live ? rsqrtf(fmaf(ss, 1.f / D, eps)) : 0.f;
-            const float f = -r * r * r * ux * (1.f / D);
+            // r^3 mean(u x) from the inside: r^3 alone leaves fp32 for rows of 1e13 or 1e-13
+            const float f = -(r * ux * (1.f / D)) * r * r;
             const uint64_t rr = f2_pack(r, r), ff = f2_pack(f, f);
 #pragma unroll
             for (int e = 0; e < P / 2; ++e) {

@@ -346,6 +346,26 @@ def test_qk_backward(hga, dtype, N, Hq, Hkv, D, r):
                        for s, t in zip(again, (dq, dk, dv, da, db)))
 
 
+@pytest.mark.parametrize("size", [1e16, 1e-16])
+@pytest.mark.parametrize("dtype,N,Hq,Hkv,D", [("f32", 5, 3, 1, 64), ("bf16", 5, 4, 2, 128)])
+def test_qk_rows_far_from_one(hga, dtype, N, Hq, Hkv, D, size):
+    """Rows whose squares fit fp32 while the cube of their inverse norm does not."""
+    _, q, k, v = qkv(N, N, Hq, Hkv, D, dtype)
+    q, k = q * size, k * size
+    qw, kw = weights(N + 1, D, dtype)
+    pos = np.arange(N) * 37
+    R, layout, w, m = rope_ref({}, D)
+    rope = hga.HGARope()
+    g = torch.Generator().manual_seed(N)
+    d = [torch.randn(N, h, D, generator=g).cuda() for h in (Hq, Hkv)]
+    y = hga.hga_qk_norm_rope(q, k, v, i32(pos), rope, q_weight=qw, k_weight=kw, eps=0.0)
+    r = hga.hga_qk_norm_rope_backward(q, k, d[0], d[1], i32(pos), rope, q_weight=qw, k_weight=kw, eps=0.0)
+    for x, dy, wt, gy, gx, gw in ((q, d[0], qw, y[0], r[0], r[3]), (k, d[1], kw, y[1], r[1], r[4])):
+        assert ref.worst(f64(gy), *ref.norm_rope(f64(x), f64(wt), pos, R, layout, w, m, 0.0, dtype)) <= 1
+        dx, dw = ref.norm_rope_grad(f64(x), f64(dy), f64(wt), pos, R, layout, w, m, 0.0, dtype)
+        assert ref.worst(f64(gx), *dx) <= 1 and ref.worst(f64(gw), *dw) <= 1
+
+
 def test_qk_backward_against_differences():
     """The formula the kernels are held to is the derivative: central differences
     of the 64-bit forward in a random direction."""
