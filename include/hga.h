@@ -360,7 +360,8 @@ hga_status hga_hostkv_plan_for(const hga_dims *dims, const hga_params *prm,
  * for hga_paged_decode also B * Hkv * max_pages * page_size (max_pages * page_size
  * at most window + sinks with a window) below 2^36.
  * int32 buffers need 4-byte alignment, rows of q, k, v, pages and gradients
- * 16-byte alignment.  Outputs must not overlap inputs except where stated. */
+ * 16-byte alignment.  Outputs must not overlap inputs except where stated, and
+ * calls that share a workspace must not overlap on the GPU. */
 typedef struct hga_paged_dims {
     int32_t B;          /* sequences: rows of the block table, of lens and of q */
     int32_t Hq, Hkv, D; /* as in hga_dims                                       */
@@ -506,7 +507,7 @@ size_t hga_qk_norm_rope_backward_workspace(const hga_dims *dims);
  * the same bits.  fp32 softmax statistics and sums; for bf16 the softmax weights
  * are rounded to bf16 for their product with the values.
  * workspace: hga_paged_decode_workspace(dims) bytes, 256-byte aligned; it needs
- * no initial value.  Calls that share a workspace must not overlap on the GPU. */
+ * no initial value. */
 hga_status hga_paged_decode(const hga_paged_dims *dims, const void *q, const void *k_pages,
                             const void *v_pages, const int32_t *block_table, const int32_t *lens,
                             int32_t window, int32_t sinks, double scale, void *out, float *lse,

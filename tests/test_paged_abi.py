@@ -193,6 +193,17 @@ def test_rope_values(lib, bad, code):
     assert call_grad(lib, tdims(), grad_io(d_q=None), rope(**bad)) == code
 
 
+def test_values_beyond_fp32(lib):
+    """What the kernels take in fp32 and would be infinite there."""
+    assert call_qk(lib, tdims(T=0), qk_io(), rope(magnitude=1e38)) == 0
+    assert call_qk(lib, tdims(T=0), qk_io(), rope(magnitude=1e39)) == INVALID
+    assert call_grad(lib, tdims(), grad_io(d_q=None), rope(magnitude=1e39)) == INVALID
+    assert call_qk(lib, tdims(), qk_io(eps=1e39)) == INVALID
+    assert call_grad(lib, tdims(), grad_io(eps=1e39)) == INVALID
+    for scale in (1e39, 3e38):              # times log2(e), as the kernel has it
+        assert decode_call(lib, pdims(), scale=scale) == INVALID
+
+
 def test_qk_pointers_and_strides(lib):
     for f in ("q", "k", "v", "pos"):
         assert call_qk(lib, tdims(), qk_io(**{f: None})) == INVALID, f
