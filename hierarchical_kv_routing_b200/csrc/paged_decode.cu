@@ -93,6 +93,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// Weights (not negative, or NaN) as sums of two bf16: hi is the largest bf16 below the
+// weight, at most 2^-7 of it short, lo the rest, rounded by at most half a step, 2^-8:
+// together 2^-15 of the weight.  Neither is zero where the weight is not, nor of
+// another sign, so that under an infinite value both give infinity.
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    const uint32_t ha = (uint32_t)max((int)__float_as_uint(a) - 1, 0) & 0xffff0000u;
+    const uint32_t hb = (uint32_t)max((int)__float_as_uint(b) - 1, 0) & 0xffff0000u;
+    hi = __byte_perm(ha, hb, 0x7632);
+    lo = pack2(a - __uint_as_float(ha), b - __uint_as_float(hb));
+}
 
 // Where chunk c (16 bytes) of merge row r lies in its row: the four rows that a
 // half-warp's 8-byte stores touch fall in different banks.
@@ -142,16 +152,20 @@ struct Walk {
 
 // ---- bf16: m16n8k16 tiles.  S = Q K^T with the queries as the 16-row A operand
 // (rows beyond the chunk's heads are zero) and K rows as its columns; the S
-// accumulator, exponentiated and rounded, is the A operand of O += P V, V read
-// transposed.  Rows of shared memory are XOR-swizzled in 16-byte chunks so the
-// eight rows of an ldmatrix fall in different banks.  kRows = 8 leaves the upper
-// half of the tile out of everything but the products; kRows = 32 is two tiles that
-// share every fragment of K and V.
+// accumulator, exponentiated and split into two bf16, is the A operand of O += P V, V
+// read transposed.  Rows of shared memory are XOR-swizzled in 16-byte chunks so the
+// eight rows of an ldmatrix fall in different banks.  The weights' lower parts are the
+// upper half of a tile of 8 rows, at no product more, and a second product of one of
+// 16 (64 x 16K tokens, one bf16 for a weight against two: 8/8 heads of 64 310 and 312
+// us, 16/1 50 and 51, 32/1 59 and 68).  kRows = 24 and 32 are two tiles that share every
+// fragment of K and V; 24 rows need the second product in one of them only (24/1 heads:
+// 61 us, 69 on 32 rows).
 template <int D, int kRows> struct TileBf16 {
     using T = __nv_bfloat16;
     static constexpr int kKeys = kTileBytes / (D * 2), kSwz = 7, kMerge = 8;
-    static constexpr int M = kRows > 16 ? kRows / 16 : 1;   // tiles
-    static constexpr int R = kRows > 8 ? 2 : 1;             // row groups of a tile in use
+    static constexpr int M = (kRows + 15) / 16, R = kRows > 8 ? 2 : 1;   // tiles; groups of 8 rows
+    // groups of tile t that are rows; where it is one, the other holds its lower parts
+    static constexpr __host__ __device__ int groups(int t) { return kRows - 16 * t > 8 ? 2 : 1; }
     uint32_t q[M][D / 16][4];
     float o[M][D / 8][4];
     float m[M][R], l[M][R];
@@ -167,7 +181,7 @@ template <int D, int kRows> struct TileBf16 {
                 for (int j = 0; j < 4; ++j) {
                     const int row = t * 16 + g + (j & 1) * 8;
                     q[t][i][j] = 0;
-                    if ((j & 1) < R && row < heads)
+                    if ((j & 1) < groups(t) && row < heads)
                         q[t][i][j] = *reinterpret_cast<const uint32_t *>(base + row * D + i * 16 + (j >> 1) * 8);
                 }
 #pragma unroll
@@ -175,7 +189,7 @@ template <int D, int kRows> struct TileBf16 {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[t][i][j] = 0.f;
 #pragma unroll
-            for (int r = 0; r < R; ++r) m[t][r] = -INFINITY, l[t][r] = 0.f;
+            for (int r = 0; r < groups(t); ++r) m[t][r] = -INFINITY, l[t][r] = 0.f;
         }
     }
 
@@ -211,18 +225,18 @@ template <int D, int kRows> struct TileBf16 {
 #pragma unroll
         for (int t = 0; t < M; ++t) {
 #pragma unroll
-            for (int r = 0; r < R; ++r) top[t][r] = -INFINITY;
+            for (int r = 0; r < groups(t); ++r) top[t][r] = -INFINITY;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int j = 0; j < 2 * R; ++j) {
+                for (int j = 0; j < 2 * groups(t); ++j) {
                     float &x = s[t][n][j];
                     x *= scale;
                     if (valid != full && !((valid >> (n * 8 + c + (j & 1))) & 1u)) x = -INFINITY;
                     top[t][j >> 1] = fmaxf(top[t][j >> 1], x);
                 }
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+            for (int r = 0; r < groups(t); ++r) {
                 top[t][r] = fmaxf(top[t][r], __shfl_xor_sync(0xffffffffu, top[t][r], 1));
                 top[t][r] = fmaxf(top[t][r], __shfl_xor_sync(0xffffffffu, top[t][r], 2));
                 // the reference moves only when the maximum passes it by 2^8: weights and
@@ -234,27 +248,26 @@ template <int D, int kRows> struct TileBf16 {
 #pragma unroll
             for (int t = 0; t < M; ++t)
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
+                for (int r = 0; r < groups(t); ++r) {
                     const float nm = top[t][r] > m[t][r] + 8.f ? top[t][r] : m[t][r];
                     const float f = nm == -INFINITY ? 1.f : ex2(m[t][r] - nm);
                     m[t][r] = nm;
                     l[t][r] *= f;
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        o[t][i][2 * r] *= f;
-                        o[t][i][2 * r + 1] *= f;
-                    }
+                    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                        for (int j = 2 * r; j < (groups(t) == 1 ? 4 : 2 * r + 2); ++j) o[t][i][j] *= f;
                 }
         }
 #pragma unroll
         for (int t = 0; t < M; ++t) {
             float ref[R];
 #pragma unroll
-            for (int r = 0; r < R; ++r) ref[r] = m[t][r] == -INFINITY ? 0.f : m[t][r];
+            for (int r = 0; r < groups(t); ++r) ref[r] = m[t][r] == -INFINITY ? 0.f : m[t][r];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int j = 0; j < 2 * R; ++j) {
+                for (int j = 0; j < 2 * groups(t); ++j) {
                     s[t][n][j] = ex2(s[t][n][j] - ref[j >> 1]);
                     l[t][j >> 1] += s[t][n][j];
                 }
@@ -262,15 +275,15 @@ template <int D, int kRows> struct TileBf16 {
         const int vrow = lane & 15, vch = lane >> 4;
 #pragma unroll
         for (int kb = 0; kb < kKeys / 16; ++kb) {
-            // the weights are rounded to bf16 (at most half a step, 2^-8 relative) for the product;
-            // their sum above is of the unrounded ones
-            uint32_t p[M][4];
+            // p: the weights' upper parts; the lower ones are in its other half with one
+            // group of rows, else in low
+            uint32_t p[M][4], low[M][4];
 #pragma unroll
             for (int t = 0; t < M; ++t)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 4; j += 3 - groups(t)) {
                     const float *x = s[t][2 * kb + (j >> 1)] + (j & 1) * 2;
-                    p[t][j] = (j & 1) < R ? pack2(x[0], x[1]) : 0u;
+                    split2(x[0], x[1], p[t][j], groups(t) == 1 ? p[t][j + 1] : low[t][j]);
                 }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -280,6 +293,10 @@ template <int D, int kRows> struct TileBf16 {
                 for (int t = 0; t < M; ++t) {
                     mma16816(o[t][2 * i], p[t], f[0], f[1]);
                     mma16816(o[t][2 * i + 1], p[t], f[2], f[3]);
+                    if (groups(t) == 2) {
+                        mma16816(o[t][2 * i], low[t], f[0], f[1]);
+                        mma16816(o[t][2 * i + 1], low[t], f[2], f[3]);
+                    }
                 }
             }
         }
@@ -289,9 +306,16 @@ template <int D, int kRows> struct TileBf16 {
 #pragma unroll
         for (int t = 0; t < M; ++t)
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+            for (int r = 0; r < groups(t); ++r) {
                 l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 1);
                 l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], 2);
+            }
+#pragma unroll
+        for (int t = 0; t < M; ++t)
+#pragma unroll
+            for (int i = 0; groups(t) == 1 && i < D / 8; ++i) {
+                o[t][i][0] += o[t][i][2];
+                o[t][i][1] += o[t][i][3];
             }
     }
     // rows round * kMerge .. + kMerge of this warp
@@ -300,7 +324,7 @@ template <int D, int kRows> struct TileBf16 {
 #pragma unroll
         for (int t = 0; t < M; ++t)
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int r = 0; r < groups(t); ++r)
                 if (t * 2 + r == round) {
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i)
@@ -893,12 +917,14 @@ hga_status launch_paged_decode(const PagedArgs &A, int dtype, int D, void *ws, c
             return S.gch > 8 ? run<TileBf16<128, 16>, 128, 16, 1>(A, S, st)
                              : run<TileBf16<128, 8>, 128, 8, 1>(A, S, st);
         if (S.hw == 2)
-            return S.gch > 16  ? run<TileBf16<64, 32>, 64, 32, 2>(A, S, st)
-                   : S.gch > 8 ? run<TileBf16<64, 16>, 64, 16, 2>(A, S, st)
-                               : run<TileBf16<64, 8>, 64, 8, 2>(A, S, st);
-        return S.gch > 16  ? run<TileBf16<64, 32>, 64, 32, 1>(A, S, st)
-               : S.gch > 8 ? run<TileBf16<64, 16>, 64, 16, 1>(A, S, st)
-                           : run<TileBf16<64, 8>, 64, 8, 1>(A, S, st);
+            return S.gch > 24   ? run<TileBf16<64, 32>, 64, 32, 2>(A, S, st)
+                   : S.gch > 16 ? run<TileBf16<64, 24>, 64, 24, 2>(A, S, st)
+                   : S.gch > 8  ? run<TileBf16<64, 16>, 64, 16, 2>(A, S, st)
+                                : run<TileBf16<64, 8>, 64, 8, 2>(A, S, st);
+        return S.gch > 24   ? run<TileBf16<64, 32>, 64, 32, 1>(A, S, st)
+               : S.gch > 16 ? run<TileBf16<64, 24>, 64, 24, 1>(A, S, st)
+               : S.gch > 8  ? run<TileBf16<64, 16>, 64, 16, 1>(A, S, st)
+                            : run<TileBf16<64, 8>, 64, 8, 1>(A, S, st);
     }
     if (D == 128)
         return S.gch > 4 ? run<TileF32<128, 8>, 128, 8, 1>(A, S, st)

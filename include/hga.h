@@ -504,8 +504,8 @@ size_t hga_qk_norm_rope_backward_workspace(const hga_dims *dims);
  * reports HGA_ERR_BOUNDS.
  * The work is split over sequences, heads and length by the lengths on the
  * device; partial results are joined in a fixed order, so the same inputs give
- * the same bits.  fp32 softmax statistics and sums; for bf16 the softmax weights
- * are rounded to bf16 for their product with the values.
+ * the same bits.  fp32 softmax statistics and sums; for bf16 a softmax weight
+ * enters its product with the values as two bf16, good to 2^-15 of it.
  * workspace: hga_paged_decode_workspace(dims) bytes, 256-byte aligned; it needs
  * no initial value. */
 hga_status hga_paged_decode(const hga_paged_dims *dims, const void *q, const void *k_pages,
