@@ -32,6 +32,7 @@
 #include <algorithm>
 
 #include "paged_internal.cuh"
+#include "paged_walk.cuh"
 #include "sm100.cuh"
 
 namespace hga {
@@ -121,7 +122,6 @@ __device__ __forceinline__ Visible visible(const PagedArgs &A, int b) {
     v.n = v.s + len - v.lo;
     return v;
 }
-__device__ __forceinline__ int units_of(int n, int uk) { return n / uk + (n % uk != 0); }
 
 // A CTA's walk over its units: the segment [k0, k1) of item (b, it) that is next.
 struct Walk {
@@ -129,10 +129,6 @@ struct Walk {
     int left;
     Visible v;
     __device__ __forceinline__ void take() { cnt = min(nu - u, left); }
-    __device__ __forceinline__ int k0(int uk) const { return u * uk; }
-    __device__ __forceinline__ int k1(int uk) const {
-        return u + cnt >= nu ? v.n : (u + cnt) * uk;
-    }
     __device__ __forceinline__ bool next(const PagedArgs &A, const Split &S, int uk) {
         left -= cnt;
         if (left <= 0) return false;
@@ -594,25 +590,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     const int page_mask = (1 << A.log2_page) - 1;
 
     // ---- producer: the next tile's page entries are read one tile ahead of its rows
-    int pk = P.k0(uk) + ksub * kKeys, pk1 = P.k1(uk);
+    auto keys = [&](const Walk &w) { return key_walk(w.u, w.cnt, w.nu, w.v.n, uk, ksub, kKw, kKeys); };
+    KeyWalk pk = keys(P);
     bool plive = true;                              // false: no tile left
     int ptok = 0, ppage = 0, phead = 0;
     bool pin = false;
     auto fetch = [&]() {
-        while (pk >= pk1) {
+        while (!pk.more()) {
             if (!P.next(A, S, uk)) {
                 plive = false;
                 return;
             }
-            pk = P.k0(uk) + ksub * kKeys;
-            pk1 = P.k1(uk);
+            pk = keys(P);
         }
-        const int key = pk + (lane & (kKeys - 1));
-        pin = key < pk1;
-        ptok = key < P.v.s ? key : key - P.v.s + P.v.lo;
+        const unsigned key = pk.key(lane & (kKeys - 1), pin);
+        ptok = (int)(key < (unsigned)P.v.s ? key : key - (unsigned)P.v.s + (unsigned)P.v.lo);
         ppage = pin ? A.table[(int64_t)P.b * A.max_pages + (ptok >> A.log2_page)] : 0;
         phead = P.it * kHw + hsub;
-        pk += kKeys * kKw;
+        pk.next();
     };
     auto issue = [&](int stage) {
         if (plive) {
@@ -651,8 +646,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
     int done = 0;                                   // units before the segment
     t.begin(A, C.b, (C.it * kHw + hsub) * A.G + g0, heads);
     for (bool more = true; more;) {
-        const int k1 = C.k1(uk), h0 = C.it * kHw, b = C.b;
-        for (int k = C.k0(uk) + ksub * kKeys; k < k1; k += kKeys * kKw) {
+        const int h0 = C.it * kHw, b = C.b;
+        for (KeyWalk k = keys(C); k.more(); k.next()) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
             __syncwarp();
             issue(stage == 0 ? kStages - 1 : stage - 1);

@@ -54,3 +54,40 @@ def test_decode_infinite_values_stay_infinite(hga, Hq, Hkv, D, sign):
         assert (out[-1, :, 3] == sign * float("inf")).all()
         rest = torch.cat([out[-1, :, :3], out[-1, :, 4:]], -1)
         assert torch.isfinite(rest).all() and torch.isfinite(out[:-1]).all()
+
+
+@pytest.mark.parametrize("dtype,D,off", [("bf16", 64, 0), ("bf16", 128, 5), ("f32", 128, 0), ("f32", 64, 17)])
+def test_decode_rows_of_the_largest_size(hga, dtype, D, off):
+    """A row within a unit of 2^31 keys (pages are shared, so it takes little memory):
+    all of it, and with a window at its far end.
+
+    The keys of the last two pages score 40, all others 0, so that these m keys make the
+    result: the n others together weigh n e^-40 < 2^-26 of one of them.  lse = 40 +
+    log(m + (n - m) e^-40): the score, its scale and the sum are a few roundings of
+    fp32 at 43 and below, less than 2^-18 40 = 1.5e-4 together, where one key more or
+    less of m <= 32 is 0.03.  The m scores are equal, so the values' mean is good to
+    2^-19 and the output's rounding."""
+    page, M = 16, (1 << 27) - 1
+    n = M * page - off
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    kp = torch.zeros(3, page, 1, D, dtype=dt, device="cuda")
+    vp = torch.ones(3, page, 1, D, dtype=dt, device="cuda")
+    kp[1:] = 8.0
+    vp[1], vp[2] = 3.0, 5.0
+    table = torch.zeros(1, M, dtype=torch.int32, device="cuda")
+    table[0, M - 2], table[0, M - 1] = 1, 2
+    q = torch.full((1, 1, D), 0.5, dtype=dt, device="cuda")
+    lens = i32([n])
+    s = 40.0
+    scale = s / (4.0 * D)                         # q.k of the last pages is 4 D
+    in1, in2 = page - max(0, off - page), page - min(off, page)
+    m = in1 + in2
+    want_lse = s + np.log(m + (n - m) * np.exp(-s))
+    want = (3.0 * in1 + 5.0 * in2) / m
+    out, lse = hga.hga_paged_decode(q, kp, vp, table, lens, scale=scale, want_lse=True)
+    assert abs(float(lse) - want_lse) <= 2 ** -18 * s
+    assert (out.double() - want).abs().max() <= (2 ** -19 + ref.STEP[dtype]) * want
+    out, lse = hga.hga_paged_decode(q, kp, vp, table, lens, scale=scale, want_lse=True, window=100, sinks=7)
+    assert abs(float(lse) - (s + np.log(m + (107 - m) * np.exp(-s)))) <= 2 ** -18 * s
+    assert (out.double() - want).abs().max() <= (2 ** -19 + ref.STEP[dtype]) * want
+    assert hga.hga_device_status() == 0
