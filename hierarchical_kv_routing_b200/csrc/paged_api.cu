@@ -215,6 +215,8 @@ hga_status hga_qk_norm_rope_backward(const hga_dims *dims, const hga_rope *rope,
         return HGA_ERR_INVALID_ARG;
     if (!aligned(io->d_q_weight, 4) || !aligned(io->d_k_weight, 4)) return HGA_ERR_INVALID_ARG;
     const bool weights = io->q_weight || io->k_weight;
+    // read for an empty batch too, whose gradients of zero the kernel writes
+    if (!aligned(io->q_weight, 16) || !aligned(io->k_weight, 16)) return HGA_ERR_INVALID_ARG;
     if (dims->T > 0) {
         if (a.rope.R && (!io->pos || !aligned(io->pos, 4))) return HGA_ERR_INVALID_ARG;
         if (!io->d_q || !io->d_k || !rows_ok(io->dq, io->dq_stride, dims->Hq, D, e) ||
@@ -223,7 +225,7 @@ hga_status hga_qk_norm_rope_backward(const hga_dims *dims, const hga_rope *rope,
             (io->q_weight && !rows_ok(io->q, io->q_stride, dims->Hq, D, e)) ||
             (io->k_weight && !rows_ok(io->k, io->k_stride, dims->Hkv, D, e)))
             return HGA_ERR_INVALID_ARG;
-        const void *rows[] = {io->d_q, io->d_k, io->d_v, io->q_weight, io->k_weight};
+        const void *rows[] = {io->d_q, io->d_k, io->d_v};
         for (const void *p : rows)
             if (!aligned(p, 16)) return HGA_ERR_INVALID_ARG;
     }

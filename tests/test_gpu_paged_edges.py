@@ -91,3 +91,20 @@ def test_decode_rows_of_the_largest_size(hga, dtype, D, off):
     assert abs(float(lse) - (s + np.log(m + (107 - m) * np.exp(-s)))) <= 2 ** -18 * s
     assert (out.double() - want).abs().max() <= (2 ** -19 + ref.STEP[dtype]) * want
     assert hga.hga_device_status() == 0
+
+
+# ---------------------------------------------------- norms and rotation --
+
+def test_qk_backward_of_no_tokens(hga):
+    """Zero gradients of the weights; weights that are not on 16 bytes are refused, as
+    with tokens."""
+    x = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(72, dtype=torch.bfloat16, device="cuda")
+    call = lambda wt: hga.hga_qk_norm_rope_backward(x, x[:, :2], x, x[:, :2], i32([]), hga.HGARope(),
+                                                    q_weight=wt, k_weight=w[8:])
+    for at in (1, 4):
+        with pytest.raises(hga.HGAError):
+            call(w[at:at + 64])
+    dq, dk, _, dqw, dkw = call(w[:64])
+    assert dq.shape == x.shape and not dqw.any() and not dkw.any()
+    assert hga.hga_device_status() == 0

@@ -285,3 +285,13 @@ def test_reference_rotation_pins():
     assert (np.diff(w / base) <= 1e-12).all()
     assert ref.visible(9, 3, 2) == [0, 1, 6, 7, 8] and ref.visible(3, 9, 2) == [0, 1, 2]
     assert ref.visible(4, 0, 2) == [0, 1, 2, 3]
+
+
+def test_qk_grad_of_no_tokens_checks_the_weights(lib):
+    """Without tokens the kernel still runs (it writes the weights' zero gradients) and
+    reads the weights in 16-byte words."""
+    for f in ("q_weight", "k_weight"):
+        for off in (2, 8):
+            assert call_grad(lib, tdims(T=0), grad_io(**{f: A + off})) == INVALID, f
+    for f in ("d_q_weight", "d_k_weight"):
+        assert call_grad(lib, tdims(T=0), grad_io(**{f: A + 2})) == INVALID, f
