@@ -3,7 +3,7 @@
 //
 //   r = (mean x^2 + eps)^(-1/2), and for a pair (a, b) of a row
 //   y_a = r (a (w_a cos) - b (w_b sin)),  y_b = r (b (w_b cos) + a (w_a sin))
-// (dimensions outside the rotated part: cos 1, sin 0): weight and rotation are one
+// (dimensions outside the rotated part: y_a = r a w_a): weight and rotation are one
 // multiply-add with constants that depend on the token alone.
 //
 // Bound by HBM: every row is read once and written once.  A warp walks tokens and
@@ -21,6 +21,7 @@
 // 231 and 193 us (6.8 TB/s).  Heads of 64 in small numbers are bound by issue, by what
 // a token costs before its rows (2 + 1 + 1 heads of 64: 36 us for 32K tokens).
 #include <algorithm>
+#include <type_traits>
 
 #include "paged_internal.cuh"
 #include "sm100.cuh"
@@ -69,7 +70,7 @@ template <int D> struct Angles {
             const unsigned long long u = (unsigned long long)(long long)p * turn[j];
             float s, c;
             sincospif((float)(int)(u >> 32) * 0x1p-31f, &s, &c);
-            // pairs outside the rotated part (rate 0) are left as they are
+            // pairs outside the rotated part: 1
             const float m = lane + 32 * j < r.R / 2 ? r.magnitude : 1.f;
             cs[lane + 32 * j] = make_float2(c * m, s * m);
         }
@@ -94,6 +95,16 @@ template <typename T, int D, bool kInter> __device__ __forceinline__ Place place
     }
     return p;
 }
+
+// What a lane's partners add to its dimensions: outside the rotated part nothing, also
+// where a partner is infinite and its product with a sine of 0 is NaN (-0, which
+// leaves every x as it is).  Where all of the head turns the kernels leave this out.
+struct Turns {
+    uint64_t keep, none;
+    __device__ __forceinline__ explicit Turns(const Place &p)
+        : keep(p.turns ? ~0ull : 0ull), none(p.turns ? 0ull : 0x8000000080000000ull) {}
+    __device__ __forceinline__ uint64_t cross(uint64_t x) const { return (x & keep) | none; }
+};
 
 // A lane's part of a row as it lies in memory: 16 bytes (fp32 gradients of bf16
 // rows: 32).
@@ -358,10 +369,10 @@ constexpr int kDepth = 3, kStep = 1024, kCtas = 148 * 2;
 
 // Two rows of a lane (at lo/hi and 512 bytes on in shared memory, N rows on in
 // memory): y = r (x A + x' B), to `to` and, where given, `also`.
-template <typename T, int D, bool kInter, bool kCheck>
+template <typename T, int D, bool kInter, bool kWhole, bool kCheck>
 __device__ __forceinline__ void two_rows(uint32_t lo, uint32_t hi, bool norm, float eps,
                                          const Pairs<Row<T, D>::P> &c, const Pairs<Row<T, D>::P> &s,
-                                         T *to, T *also, int skip, bool live0, bool live1) {
+                                         const Turns &turns, T *to, T *also, int skip, bool live0, bool live1) {
     using W = Row<T, D>;
     constexpr int P = W::P;
     Pairs<P> x[2];
@@ -397,8 +408,9 @@ __device__ __forceinline__ void two_rows(uint32_t lo, uint32_t hi, bool norm, fl
         Pairs<P> y;
 #pragma unroll
         for (int e = 0; e < P / 2; ++e) {
-            y.a[e] = f2_mul(f2_fma(x[u].a[e], c.a[e], f2_mul(x[u].b[e], s.a[e])), rr);
-            y.b[e] = f2_mul(f2_fma(x[u].b[e], c.b[e], f2_mul(x[u].a[e], s.b[e])), rr);
+            const uint64_t a = f2_mul(x[u].b[e], s.a[e]), b = f2_mul(x[u].a[e], s.b[e]);
+            y.a[e] = f2_mul(f2_fma(x[u].a[e], c.a[e], kWhole ? a : turns.cross(a)), rr);
+            y.b[e] = f2_mul(f2_fma(x[u].b[e], c.b[e], kWhole ? b : turns.cross(b)), rr);
         }
         const Raw<T, P> z = pack<T, P, kInter>(y);
         if (!kCheck || (u ? live1 : live0)) {
@@ -426,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_norm_rope(const QkArgs A, co
     const uint32_t ring = sm100::smem_addr(ring_all) + warp * kDepth * kStep, mine = ring + lane * 16;
     float2 *cs = cs_all[warp];
     const Place pl = place<T, D, kInter>(A.rope.R);
+    const Turns turns(pl);
     const uint32_t lo = ring + (sub * D + pl.lo) * E, hi = ring + (sub * D + pl.hi) * E;
     const float eps = (float)A.io.eps;
 
@@ -555,18 +568,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_norm_rope(const QkArgs A, co
                 }
             }
             const int skip = pl.hi - pl.lo;
-            for (int n = full; n > 0; --n) {
-                step();
-                two_rows<T, D, kInter, false>(lo + at, hi + at, norm, eps, ct, st, to, also, skip, true, true);
-                done();
-                to += N2 * D;
-                if (also) also += N2 * D;
-            }
-            if (ragged) {
-                step();
-                two_rows<T, D, kInter, true>(lo + at, hi + at, norm, eps, ct, st, to, also, skip, live0, live1);
-                done();
-            }
+            auto rows = [&](auto whole) {
+                constexpr bool W = decltype(whole)::value;
+                for (int n = full; n > 0; --n) {
+                    step();
+                    two_rows<T, D, kInter, W, false>(lo + at, hi + at, norm, eps, ct, st, turns, to, also,
+                                                     skip, true, true);
+                    done();
+                    to += N2 * D;
+                    if (also) also += N2 * D;
+                }
+                if (ragged) {
+                    step();
+                    two_rows<T, D, kInter, W, true>(lo + at, hi + at, norm, eps, ct, st, turns, to, also,
+                                                    skip, live0, live1);
+                    done();
+                }
+            };
+            if (A.rope.R == D) rows(std::true_type{});
+            else rows(std::false_type{});
         }
     }
     cp_wait<0>();
@@ -598,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
     const uint32_t ring = sm100::smem_addr(ring_all) + warp * kGradDepth * S;
     float2 *cs = cs_all[warp];
     const Place pl = place<T, D, kInter>(A.rope.R);
+    const Turns turns(pl);
     const float eps = (float)A.io.eps;
     // a lane's words of a step's slot: x at 0, dy at 512
     const uint32_t xlo = ring + (sub * D + pl.lo) * E, xhi = ring + (sub * D + pl.hi) * E;
@@ -674,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
     auto done = [&]() { at = at == (kGradDepth - 1) * S ? 0 : at + S; };
     uint64_t cc[P / 2], tt[P / 2], tn[P / 2];
     // one row of a lane; live: it exists (a ragged last step's others are zeros)
-    auto row = [&](const Pairs<P> &w, bool norm, T *out, bool live, Pairs<P> &sum) {
+    auto row = [&](auto whole, const Pairs<P> &w, bool norm, T *out, bool live, Pairs<P> &sum) {
         step();
         Raw<G, P> graw;
         read_raw<G, P, kInter>(graw, glo + at, ghi + at);
@@ -682,8 +703,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
         Pairs<P> g;
 #pragma unroll
         for (int e = 0; e < P / 2; ++e) {
-            g.a[e] = f2_fma(d.a[e], cc[e], f2_mul(d.b[e], tt[e]));
-            g.b[e] = f2_fma(d.b[e], cc[e], f2_mul(d.a[e], tn[e]));
+            const uint64_t a = f2_mul(d.b[e], tt[e]), b = f2_mul(d.a[e], tn[e]);
+            g.a[e] = f2_fma(d.a[e], cc[e], decltype(whole)::value ? a : turns.cross(a));
+            g.b[e] = f2_fma(d.b[e], cc[e], decltype(whole)::value ? b : turns.cross(b));
         }
         if (norm) {
             Raw<T, P> raw;
@@ -752,11 +774,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_qk_grad(const QkGradArgs A, con
             if (kind < 2) {
                 const Pairs<P> w = unpack<T, P, kInter>(wraw[kind]);
                 const bool norm = K.weight[kind] != nullptr;
-                for (; full > 0; --full) {
-                    row(w, norm, out, true, kind ? sumk : sumq);
-                    out += W::N * D;
-                }
-                if (ragged) row(w, norm, out, exists, kind ? sumk : sumq);
+                auto rows = [&](auto whole) {
+                    for (; full > 0; --full) {
+                        row(whole, w, norm, out, true, kind ? sumk : sumq);
+                        out += W::N * D;
+                    }
+                    if (ragged) row(whole, w, norm, out, exists, kind ? sumk : sumq);
+                };
+                if (A.rope.R == D) rows(std::true_type{});
+                else rows(std::false_type{});
                 continue;
             }
             for (int n = full + ragged; n > 0; --n, --full) {   // values: rounded to T

@@ -108,3 +108,42 @@ def test_qk_backward_of_no_tokens(hga):
     dq, dk, _, dqw, dkw = call(w[:64])
     assert dq.shape == x.shape and not dqw.any() and not dkw.any()
     assert hga.hga_device_status() == 0
+
+
+def same_bits(a, b):
+    """Equal, signs of zero included; NaN where the other is."""
+    nan = a.isnan() & b.isnan()
+    return bool((((a == b) & (a.signbit() == b.signbit())) | nan).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,R", [(64, 0), (64, 16), (64, 48), (128, 0), (128, 32), (128, 112)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_qk_unrotated_dimensions_pass_through(hga, dtype, D, R, layout):
+    """Without a norm the dimensions from rotary_dim on come out as they went in,
+    infinity, NaN and -0 included, and reach no other; with one, an infinite value makes
+    its row's mean square infinite: 0 everywhere (x times 0) but NaN at itself.  The
+    gradient likewise passes what comes in."""
+    g = torch.Generator().manual_seed(D + R)
+    x = torch.randn(9, 3, D, generator=g).to(dtype).cuda()
+    odd = x.clone()
+    odd[0, 0, R], odd[1, 1, D - 1], odd[2, 2, R + 5] = float("inf"), -float("inf"), float("nan")
+    odd[3, :, R:] = -0.0
+    odd[4, 0, R + 2:D] = float("inf")
+    pos = i32(np.arange(9) * 1000 + 1)
+    rope = hga.HGARope(rotary_dim=R, layout=layout)
+    run = lambda t, **kw: hga.hga_qk_norm_rope(t, t, t, pos, rope, **kw)
+    clean, got = run(x), run(odd)
+    for a, b, v in zip(got[:2], clean[:2], (odd, odd)):
+        assert same_bits(a[..., R:], v[..., R:])
+        assert same_bits(a[..., :R], b[..., :R])
+    back = lambda d: hga.hga_qk_norm_rope_backward(x, x, d, d, pos, rope)[:2]
+    for a, b in zip(back(odd), back(x)):
+        assert same_bits(a[..., R:], odd[..., R:])
+        assert same_bits(a[..., :R], b[..., :R])
+    w = torch.ones(D, dtype=dtype, device="cuda")
+    for a in run(odd, q_weight=w, k_weight=w)[:2]:
+        assert same_bits(a[5:], run(x, q_weight=w, k_weight=w)[0][5:])
+        for t, h in ((0, 0), (1, 1), (4, 0)):
+            inf = odd[t, h].isinf()
+            assert a[t, h][inf].isnan().all() and (a[t, h][~inf] == 0).all()
