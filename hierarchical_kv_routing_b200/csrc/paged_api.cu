@@ -18,8 +18,9 @@ int sm_count() {
 namespace {
 
 inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-// finite in the fp32 that the kernels take it in
-inline bool finite32(double x) { return std::isfinite((float)x); }
+// held by the fp32 that the kernels take it in: 0, or a normal number there.  (An eps that
+// became 0 would make a row of zeros NaN, a magnitude that did so a rotated part of 0.)
+inline bool held32(double x) { return x == 0.0 || std::isnormal((float)x); }
 inline size_t esize(int dtype) { return dtype == HGA_BF16 ? 2 : 4; }
 
 hga_status check_pages(const hga_paged_dims *d) {
@@ -64,7 +65,7 @@ hga_status form_rope(const hga_rope *r, int D, PairRope *out) {
     const int R = out->R = r->rotary_dim;
     if (R == 0) return HGA_OK;
     if (!(r->theta > 1.0) || !std::isfinite(r->theta)) return HGA_ERR_INVALID_ARG;
-    if (!finite32(r->magnitude) || r->magnitude < 0.0) return HGA_ERR_INVALID_ARG;
+    if (!held32(r->magnitude) || r->magnitude < 0.0) return HGA_ERR_INVALID_ARG;
     const bool yarn = r->scaling == HGA_ROPE_YARN;
     if (r->scaling != HGA_ROPE_UNSCALED && r->scaling != HGA_ROPE_LINEAR && !yarn)
         return HGA_ERR_INVALID_ARG;
@@ -170,7 +171,7 @@ hga_status hga_qk_norm_rope(const hga_dims *dims, const hga_rope *rope, const hg
     if (dims->T == 0) return HGA_OK;
     const size_t e = esize(dims->dtype);
     const int D = dims->D;
-    if (!(io->eps >= 0.0) || !finite32(io->eps)) return HGA_ERR_INVALID_ARG;
+    if (!(io->eps >= 0.0) || !held32(io->eps)) return HGA_ERR_INVALID_ARG;
     if (a.rope.R && (!io->pos || !aligned(io->pos, 4))) return HGA_ERR_INVALID_ARG;
     const bool wk = io->k_out || io->k_pages, wv = io->v_out || io->v_pages;
     if ((io->q_out && !rows_ok(io->q, io->q_stride, dims->Hq, D, e)) ||
@@ -209,7 +210,7 @@ hga_status hga_qk_norm_rope_backward(const hga_dims *dims, const hga_rope *rope,
     const size_t e = esize(dims->dtype);
     const int D = dims->D;
     if (io->grad_dtype != HGA_F32 && io->grad_dtype != dims->dtype) return HGA_ERR_INVALID_ARG;
-    if (!(io->eps >= 0.0) || !finite32(io->eps)) return HGA_ERR_INVALID_ARG;
+    if (!(io->eps >= 0.0) || !held32(io->eps)) return HGA_ERR_INVALID_ARG;
     if (!io->q_weight != !io->d_q_weight || !io->k_weight != !io->d_k_weight ||
         !io->d_v != !io->dv)
         return HGA_ERR_INVALID_ARG;
@@ -260,7 +261,7 @@ hga_status hga_paged_decode(const hga_paged_dims *dims, const void *q, const voi
     for (const void *p : rows)
         if (!aligned(p, 16)) return HGA_ERR_INVALID_ARG;
     if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(lse, 4)) return HGA_ERR_INVALID_ARG;
-    if (window < 0 || sinks < 0 || !(scale >= 0.0) || !finite32(scale * M_LOG2E))
+    if (window < 0 || sinks < 0 || !(scale >= 0.0) || !held32(scale * M_LOG2E))
         return HGA_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) ||
         workspace_bytes < paged_decode_workspace_bytes(dims->B, dims->Hq, dims->Hkv, dims->D,

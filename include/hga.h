@@ -359,6 +359,8 @@ hga_status hga_hostkv_plan_for(const hga_dims *dims, const hga_params *prm,
  * page_size and B * max_pages below 2^31; B and Hq at most 65535; D 64 or 128;
  * for hga_paged_decode also B * Hkv * max_pages * page_size (max_pages * page_size
  * at most window + sinks with a window) below 2^36.
+ * eps, magnitude and scale are taken in fp32: 0 or a normal number there (about 1.2e-38
+ * to 3.4e38; scale times log2 e).
  * int32 buffers need 4-byte alignment, rows of q, k, v, pages and gradients
  * 16-byte alignment.  Outputs must not overlap inputs except where stated, and
  * calls that share a workspace must not overlap on the GPU. */

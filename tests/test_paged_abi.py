@@ -295,3 +295,19 @@ def test_qk_grad_of_no_tokens_checks_the_weights(lib):
             assert call_grad(lib, tdims(T=0), grad_io(**{f: A + off})) == INVALID, f
     for f in ("d_q_weight", "d_k_weight"):
         assert call_grad(lib, tdims(T=0), grad_io(**{f: A + 2})) == INVALID, f
+
+
+def test_values_below_fp32(lib):
+    """What fp32 holds as 0 or with fewer bits (below 2^-126): an eps of 0 would make a
+    row of zeros NaN, a magnitude of 0 its rotated part 0.  0 itself and 2^-126 are taken."""
+    for bad in (1e-50, 5e-324, 1e-45, 2.0 ** -127):
+        assert call_qk(lib, tdims(T=0), qk_io(), rope(magnitude=bad)) == INVALID
+        assert call_grad(lib, tdims(), grad_io(d_q=None), rope(magnitude=bad)) == INVALID
+        assert call_qk(lib, tdims(), qk_io(eps=bad)) == INVALID
+        assert call_grad(lib, tdims(), grad_io(eps=bad)) == INVALID
+        assert decode_call(lib, pdims(), scale=bad) == INVALID
+    for good in (0.0, 2.0 ** -126):
+        assert call_qk(lib, tdims(T=0), qk_io(), rope(magnitude=good)) == 0
+        assert call_grad(lib, tdims(), grad_io(eps=good, d_q_weight=A + 2)) == INVALID
+        assert decode_call(lib, pdims(), scale=good, ws=None) == WORKSPACE
+        assert call_grad(lib, tdims(), grad_io(eps=good), ws=None) == WORKSPACE
