@@ -81,6 +81,9 @@ hga_status form_rope(const hga_rope *r, int D, PairRope *out) {
         };
         lo = std::fmax(std::floor(dim(r->beta_fast)), 0.0);
         hi = std::fmin(std::ceil(dim(r->beta_slow)), (double)(R - 1));
+        // every pair on one side of the ramp (a trained length of a few tokens, or of more
+        // turns than any pair has): the ramp would run backwards
+        if (hi < lo) return HGA_ERR_INVALID_ARG;
         if (hi == lo) hi = lo + 0.001;
         magnitude = 0.1 * std::log(r->factor) + 1.0;
     }

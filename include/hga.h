@@ -429,6 +429,7 @@ typedef enum hga_rope_scaling {
  *          min(R - 1, ceil(d(beta_slow))) (hi = lo + 0.001 if equal), d(t) =
  *          R ln(original_len / (2 pi t)) / (2 ln theta): pairs that turn more
  *          than beta_fast times over the original length keep their rate.
+ *          hi < lo (all pairs on one side of the ramp) is refused.
  * The rotated part is multiplied by `magnitude`; 0 selects 1, for YARN
  * 0.1 ln(factor) + 1. */
 typedef struct hga_rope {

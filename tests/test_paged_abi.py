@@ -311,3 +311,21 @@ def test_values_below_fp32(lib):
         assert call_grad(lib, tdims(), grad_io(eps=good, d_q_weight=A + 2)) == INVALID
         assert decode_call(lib, pdims(), scale=good, ws=None) == WORKSPACE
         assert call_grad(lib, tdims(), grad_io(eps=good), ws=None) == WORKSPACE
+
+
+def test_yarn_ramp_that_would_run_backwards(lib):
+    """lo and hi by the header's formula: where hi < lo, pairs that turn often would be
+    slowed and the others not.  hi = lo and a first or last pair on the ramp are taken."""
+    def ends(theta, L, fast, slow, R=64):
+        d = lambda t: R * np.log(L / (2 * np.pi * t)) / (2 * np.log(theta))
+        return max(0.0, np.floor(d(fast))), min(R - 1.0, np.ceil(d(slow)))
+    seen = set()
+    for theta, L, fast, slow in [(1e6, 3, 32.0, 1.0), (1e6, 6, 32.0, 1.0), (1e6, 7, 32.0, 1.0),
+                                 (10.0, 1 << 20, 32.0, 1.0), (10.0, 1 << 14, 32.0, 1.0), (1e4, 4096, 32.0, 1.0),
+                                 (1e4, 4096, 1e9, 1e9), (1e4, 100, 16.0, 15.0), (1e4, 4096, 4.0, 4.0)]:
+        lo, hi = ends(theta, L, fast, slow)
+        r = rope(scaling=2, factor=4.0, theta=theta, original_len=L, beta_fast=fast, beta_slow=slow)
+        want = INVALID if hi < lo else 0
+        assert call_qk(lib, tdims(T=0), qk_io(), r) == want, (theta, L, lo, hi)
+        seen.add(want)
+    assert seen == {0, INVALID}
