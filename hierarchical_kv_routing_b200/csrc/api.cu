@@ -1,6 +1,7 @@
 // The C ABI of include/hga.h: host-side argument checks, workspace layout and
 // kernel dispatch.  Nothing here allocates device memory; every kernel is
 // enqueued on the caller's stream.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -54,7 +55,24 @@ hga_status set_rope(Rope *r, int D, double theta, double hf_wavelength, int C) {
     return HGA_OK;
 }
 
+// The first error word that is set, into a call's slot (calls on several streams at once
+// each have their own), and the words reset: one launch and one copy, 20 us a call (a
+// copy for each of the eight words: 76).
+constexpr int kErrorWords = 8, kStatusSlots = 1024;
+__device__ int g_status[kStatusSlots];
+
 namespace {
+
+struct ErrorWords {
+    int *at[kErrorWords];
+};
+__global__ void k_first_error(ErrorWords words, int clear, unsigned slot) {
+    const int i = threadIdx.x;
+    const int v = i < kErrorWords ? (clear ? atomicExch(words.at[i], 0) : atomicAdd(words.at[i], 0)) : 0;
+    const unsigned set = __ballot_sync(0xffffffffu, v != 0);
+    const int first = __shfl_sync(0xffffffffu, v, set ? __ffs((int)set) - 1 : 0);
+    if (i == 0) g_status[slot] = first;
+}
 
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -362,18 +380,24 @@ int hga_last_cuda_error(void) { return g_last_cuda_error; }
 
 hga_status hga_device_status(void *stream, int clear) {
     const cudaStream_t st = (cudaStream_t)stream;
-    hga_status first = HGA_OK;
-    const hga_status parts[8] = {summaries_error_take(st, clear != 0),
-                                 attend_tc_error_take(st, clear != 0),
-                                 decode_error_take(st, clear != 0),
-                                 tier_error_take(st, clear != 0),
-                                 backward_error_take(st, clear != 0),
-                                 plan_error_take(st, clear != 0),
-                                 qk_error_take(st, clear != 0),
-                                 paged_error_take(st, clear != 0)};
-    for (hga_status p : parts)
-        if (p != HGA_OK && first == HGA_OK) first = p;
-    return first;
+    static std::atomic<unsigned> calls{0};
+    ErrorWords words;
+    cudaError_t (*const of[kErrorWords])(int **) = {
+        summaries_error_word, attend_tc_error_word, decode_error_word, tier_error_word,
+        backward_error_word,  plan_error_word,      qk_error_word,     paged_error_word};
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < kErrorWords && e == cudaSuccess; ++i) e = of[i](&words.at[i]);
+    const unsigned slot = calls.fetch_add(1) % kStatusSlots;
+    int first = 0;
+    if (e == cudaSuccess) {
+        k_first_error<<<1, 32, 0, st>>>(words, clear, slot);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess)
+        e = cudaMemcpyFromSymbolAsync(&first, g_status, sizeof(int), slot * sizeof(int),
+                                      cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    return e == cudaSuccess ? (hga_status)first : cuda_status(e);
 }
 
 hga_status hga_set_test_hooks(int skip_summaries_copy, unsigned long long summaries_wait_ns,

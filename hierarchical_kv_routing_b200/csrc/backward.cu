@@ -1104,17 +1104,6 @@ hga_status launch_attend_backward(const Geo &g, const Rope &r, int dtype, const 
                                            dout, dq, dk, dv, ws, q_rot, st);
 }
 
-hga_status backward_error_take(cudaStream_t st, bool clear) {
-    int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_bwd_error, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && clear && v) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_bwd_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    }
-    if (e != cudaSuccess) return cuda_status(e);
-    return (hga_status)v;
-}
+cudaError_t backward_error_word(int **word) { return cudaGetSymbolAddress((void **)word, g_bwd_error); }
 
 }  // namespace hga

@@ -187,15 +187,15 @@ hga_status launch_attend_backward(const Geo &g, const Rope &r, int dtype, const 
                                   const int32_t *sel_group, const float *lse,
                                   const void *dout, float *dq, float *dk, float *dv, void *ws,
                                   const void *q_rot, cudaStream_t st);
-hga_status backward_error_take(cudaStream_t st, bool clear);
 
-// Device error words (bounded-wait timeouts, bounds checks) of each kernel
-// file: read on a stream after its queued work, optionally reset.
-hga_status attend_tc_error_take(cudaStream_t st, bool clear);
-hga_status decode_error_take(cudaStream_t st, bool clear);
-hga_status summaries_error_take(cudaStream_t st, bool clear);
+// Where the current device holds the error word (bounded-wait timeouts, bounds
+// checks) of each kernel file.
+cudaError_t summaries_error_word(int **word);
+cudaError_t attend_tc_error_word(int **word);
+cudaError_t decode_error_word(int **word);
+cudaError_t tier_error_word(int **word);
+cudaError_t backward_error_word(int **word);
 hga_status summaries_test_hooks(int skip_copy, unsigned long long wait_ns, cudaStream_t st);
-hga_status tier_error_take(cudaStream_t st, bool clear);
 hga_status tier_link_bytes_take(cudaStream_t st, unsigned long long *bytes, bool clear);
 
 // Decode step (append, close-chunk summaries, route, split attention).

@@ -928,8 +928,6 @@ hga_status launch_paged_decode(const PagedArgs &A, int dtype, int D, void *ws, c
                      : run<TileF32<64, 4>, 64, 4, 1>(A, S, st);
 }
 
-hga_status paged_error_take(cudaStream_t st, bool clear) {
-    return take_error_word(g_paged_error, st, clear);
-}
+cudaError_t paged_error_word(int **word) { return cudaGetSymbolAddress((void **)word, g_paged_error); }
 
 }  // namespace hga

@@ -56,25 +56,9 @@ hga_status launch_qk_norm_rope_backward(const QkGradArgs &a, int dtype, int D, c
 size_t paged_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int dtype);
 hga_status launch_paged_decode(const PagedArgs &a, int dtype, int D, void *ws, cudaStream_t st);
 
-hga_status plan_error_take(cudaStream_t st, bool clear);
-hga_status qk_error_take(cudaStream_t st, bool clear);
-hga_status paged_error_take(cudaStream_t st, bool clear);
-
-// Reads a kernel file's error word on `st` after the queued work, optionally
-// resets it, and returns the recorded status.
-template <typename Word>
-hga_status take_error_word(Word &word, cudaStream_t st, bool clear) {
-    int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, word, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && clear && v) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(word, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    }
-    if (e != cudaSuccess) return cuda_status(e);
-    return (hga_status)v;
-}
+cudaError_t plan_error_word(int **word);
+cudaError_t qk_error_word(int **word);
+cudaError_t paged_error_word(int **word);
 
 // Launch as a programmatic dependent of whatever precedes on the stream: the grid may
 // start when that kernel's CTAs have all allowed it (or ended), and every kernel

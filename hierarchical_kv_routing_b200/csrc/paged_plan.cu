@@ -231,8 +231,6 @@ hga_status launch_paged_plan(const PlanArgs &a, cudaStream_t st) {
                                         dim3(256), 0, st, a));
 }
 
-hga_status plan_error_take(cudaStream_t st, bool clear) {
-    return take_error_word(g_plan_error, st, clear);
-}
+cudaError_t plan_error_word(int **word) { return cudaGetSymbolAddress((void **)word, g_plan_error); }
 
 }  // namespace hga

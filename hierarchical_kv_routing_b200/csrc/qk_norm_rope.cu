@@ -932,6 +932,6 @@ hga_status launch_qk_norm_rope_backward(const QkGradArgs &a, int dtype, int D, c
                     : backward<__nv_bfloat16, __nv_bfloat16, 64>(a, st);
 }
 
-hga_status qk_error_take(cudaStream_t st, bool clear) { return take_error_word(g_qk_error, st, clear); }
+cudaError_t qk_error_word(int **word) { return cudaGetSymbolAddress((void **)word, g_qk_error); }
 
 }  // namespace hga

@@ -651,18 +651,6 @@ hga_status tier_link_bytes_take(cudaStream_t st, unsigned long long *bytes, bool
     return HGA_OK;
 }
 
-// Reads this file's device error word on `st` and optionally resets it.
-hga_status tier_error_take(cudaStream_t st, bool clear) {
-    int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_tier_error, sizeof(int), 0, cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    if (e == cudaSuccess && clear && v) {
-        const int zero = 0;
-        e = cudaMemcpyToSymbolAsync(g_tier_error, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, st);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    }
-    if (e != cudaSuccess) return cuda_status(e);
-    return (hga_status)v;
-}
+cudaError_t tier_error_word(int **word) { return cudaGetSymbolAddress((void **)word, g_tier_error); }
 
 }  // namespace hga

@@ -147,3 +147,50 @@ def test_qk_unrotated_dimensions_pass_through(hga, dtype, D, R, layout):
         for t, h in ((0, 0), (1, 1), (4, 0)):
             inf = odd[t, h].isinf()
             assert a[t, h][inf].isnan().all() and (a[t, h][~inf] == 0).all()
+
+
+# ---------------------------------------------------------------- status --
+
+def test_device_status_of_several_operators(hga):
+    """One status for every kernel's word: kept until it is cleared, cleared as a whole."""
+    def bad_plan():
+        hga.hga_paged_plan(i32([-1]), i32([1]), i32([0] * 4), i32([4]), i32([[0]]), 4, 1)
+
+    def bad_slot():
+        x = torch.zeros(1, 1, 64, device="cuda")
+        kp = torch.zeros(1, 4, 1, 64, device="cuda")
+        hga.hga_qk_norm_rope(x, x, x, i32([0]), hga.HGARope(), k_pages=kp, v_pages=kp.clone(), slot=i32([4]))
+
+    def bad_length():
+        kp, vp, table = pages_for(1, [4], 1, 64, "f32", 4)
+        hga.hga_paged_decode(queries(1, 1, 1, 64, "f32"), kp, vp, table, i32([99]))
+    assert hga.hga_device_status() == 0
+    for calls in ((bad_plan,), (bad_slot,), (bad_length,), (bad_plan, bad_slot, bad_length)):
+        for f in calls:
+            f()
+        assert hga.hga_device_status(clear=False) == 5
+        assert hga.hga_device_status(clear=False) == 5
+        assert hga.hga_device_status() == 5 and hga.hga_device_status() == 0
+    other = torch.cuda.Stream()
+    bad_slot()
+    torch.cuda.synchronize()
+    assert hga.hga_device_status(stream=other) == 5 and hga.hga_device_status() == 0
+    for _ in range(1100):                          # more calls than there are places for a result
+        assert hga.hga_device_status(clear=False) == 0
+
+
+def test_device_status_takes_one_read(hga):
+    """A launch and a copy, not a copy for every kernel file's word: against the read of
+    one value, which is a copy (measured 2 times; with a copy a word 8)."""
+    import time
+    x = torch.zeros(1, device="cuda")
+
+    def median(f):
+        t = []
+        for _ in range(300):
+            t0 = time.perf_counter()
+            f()
+            t.append(time.perf_counter() - t0)
+        return sorted(t)[150]
+    median(hga.hga_device_status)
+    assert min(median(hga.hga_device_status) / median(x.item) for _ in range(3)) < 4
