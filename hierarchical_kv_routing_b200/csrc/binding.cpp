@@ -141,6 +141,11 @@ double real(PyObject *o) {
     if (x == -1.0 && PyErr_Occurred()) throw Raised();
     return x;
 }
+bool truth(PyObject *o) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) throw Raised();
+    return x > 0;
+}
 int32_t size32(int64_t x, const char *name) {
     if (x > INT32_MAX) refuse(name, " of ", x, " is beyond 2^31 - 1");
     return (int32_t)x;
@@ -446,7 +451,7 @@ PyObject *decode(PyObject *const *a) {
     const double scale = real(a[7]);
     const at::Tensor out = output(a[8], "out", {B, Hq, D}, dt, c);
     at::Tensor lse, keep;
-    if (!none(a[10]) || PyObject_IsTrue(a[9])) lse = output(a[10], "lse", {B, Hq}, at::kFloat, c);
+    if (!none(a[10]) || truth(a[9])) lse = output(a[10], "lse", {B, Hq}, at::kFloat, c);
     size_t bytes = 0;
     void *ws = workspace(a[11], hga_paged_decode_workspace(&d), c, keep, bytes);
     check(hga_paged_decode(&d, pq, pk, pv, pt, pl, window, sinks, scale, out.data_ptr(),

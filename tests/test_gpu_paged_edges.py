@@ -194,3 +194,9 @@ def test_device_status_takes_one_read(hga):
         return sorted(t)[150]
     median(hga.hga_device_status)
     assert min(median(hga.hga_device_status) / median(x.item) for _ in range(3)) < 4
+
+
+def test_an_argument_without_a_truth_value_raises_its_own_error(hga):
+    kp, vp, table = pages_for(1, [4], 1, 64, "bf16", 4)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        hga.hga_paged_decode(queries(1, 1, 1, 64, "bf16"), kp, vp, table, i32([4]), want_lse=torch.zeros(2))
