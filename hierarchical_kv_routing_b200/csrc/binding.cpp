@@ -1,9 +1,9 @@
 // Python binding of the paged-cache operators (module _paged).
 //
 // A serving step calls these once per layer on a few tokens, where the kernels take
-// a few microseconds and a binding written in Python ten times that (measured: 21
-// us of checks and marshalling for the attention of one step, 45 for the norms'
-// gradient).  So the checks of tensors, the allocation of outputs and workspace and
+// a few microseconds and a binding written in Python ten times that (measured, at its
+// leanest: 21 us of checks and marshalling for the attention of one step, 46 for the
+// norms' gradient; here 7 and 9).  So the checks of tensors, the allocation of outputs and workspace and
 // the call of the C ABI are here; paged.py holds the signatures and the
 // documentation.  Refusals raise HGAError with the package's wording.
 #include <Python.h>

@@ -4,11 +4,15 @@
 //   j < len, and with a window w only j >= len - w or j < sinks.
 //
 // Bound by HBM: a visible key costs 2 D e bytes of K and V per KV head and
-// 4 D G FLOP, G FLOP per byte for bf16.  So every K and V row is read once for
-// all G query heads of its KV head, the products run on warp-level tensor-core
-// tiles (a new token has at most 16 rows of queries per KV head, below the
-// 64- and 128-row tiles of tcgen05), and the design is about keeping loads in
-// flight and every SM equally loaded.
+// 4 D G FLOP, G FLOP per byte for bf16.  So every K and V row is read once for the
+// query heads that a CTA takes: 16 of bf16 heads of 128, 32 of 64, 8 of fp32; of a
+// larger group G each chunk of that many reads K and V again, from L2.  bf16 products
+// run on warp-level tensor-core tiles with the query heads as rows, whose operands a
+// warp takes from its own ring without meeting the others; they fill a fifth of the
+// tensor pipe up to 16 heads.  (On tcgen05 the keys would have to be the 64 or 128
+// rows, as a group is fewer; for groups above 16, which are bound by issue here, that
+// has not been built.)  fp32 products run on CUDA cores.  The design is about keeping
+// loads in flight and every SM equally loaded.
 //
 // The visible tokens of a row are numbered 0 .. n-1 without a gap: the first
 // min(sinks, lo) and then lo .. len-1, lo = max(0, len - window).  Tiles, splits
@@ -726,9 +730,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_decode(const PagedArgs A,
 // dependent of k_paged_decode.  grid: (possible split items, rows).  Latency
 // bound: an item of up to kFew parts is joined by its first CTA, a group of D / 4
 // lanes per row and four parts loaded at a time; beyond that every row has its
-// CTA, whose groups share the parts.  (Whole calls: 96 rows of 640 keys, 384 items of
-// 2 or 3 parts, 23 us, 31 with a CTA per row; 1 x 32K, 4 items of 74 parts, 15 us, 28
-// with a CTA per item.)
+// CTA, whose groups share the parts.  (Whole calls, caches cold: 96 rows of 640 keys,
+// 384 items of 2 or 3 parts, 32 us, 40 with a CTA per row; 1 x 32K, 4 items of 74
+// parts, 20.5 us, 32.7 with a CTA per item; fp32 5 x 2K, 20 items of up to 15 parts,
+// 11.3 and 10.4.)
 constexpr int kJoinThreads = 256, kAhead = 8, kFew = 16;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) k_paged_join(const PagedArgs A, const Split S) {

@@ -862,9 +862,15 @@ void set_work(QkWork &K, int N, int64_t tokens) {
         steps += K.steps[i];
     }
     // Few tokens are spread over several warps each, up to four warps per SM and down
-    // to one step a warp; every warp forms the angles again.  32 + 4 + 4 heads of 128,
-    // forward: 16 tokens 3.8 us (a warp per token: 6.2), 256 4.9 (6.4), 1024 6.5; with
-    // up to sixteen warps per SM 256 5.7, 1024 9.0.
+    // to one step a warp; every warp forms the angles again.  Spread / a warp per token /
+    // spread up to sixteen warps per SM, us:
+    //                              16 tokens          256                512
+    //   32 + 4 + 4 bf16 x 128   3.6 / 6.3 / 3.6   4.9 / 6.4 / 5.9   5.5 / 6.5 / 6.4
+    //     gradient (fp32 dy)    5.2 /10.7 / 5.2   8.0 /11.3 / 8.8   9.4 /11.7 /11.4
+    //   2 + 1 + 1 bf16 x 64     3.0 / 3.5 / 3.0   3.3 / 3.6 / 3.2   3.6 / 3.7 / 3.9
+    //     gradient              4.4 / 4.7 / 4.4   5.3 / 5.3 / 5.3   5.3 / 5.5 / 6.0
+    //   8 + 8 + 8 fp32 x 64     3.0 / 4.1 / 3.0   3.4 / 4.2 / 3.8   4.1 / 4.3 / 4.6
+    //     gradient              4.4 / 6.5 / 4.4   5.9 / 6.8 / 6.8   6.4 / 7.2 / 7.5
     const int64_t want = 148 * 4;
     K.split = tokens == 0 ? 1 : (int)std::min<int64_t>(std::max(steps, 1), std::max<int64_t>(1, (want + tokens - 1) / tokens));
     K.warps = (unsigned)(tokens * K.split);

@@ -3,7 +3,10 @@ per-head norms with the position rotation and its gradient (hga_qk_norm_rope,
 hga_qk_norm_rope_backward), and attention of one new token over the pages
 (hga_paged_decode).
 
-A serving step of a layer that attends over every cached token (or a window):
+A serving step of a layer that attends over every cached token (or a window), with
+one new token in every row, so that row b of q is sequence b (the attention takes one
+token a sequence: plan and norms lay out whole prompts, but attention of a prompt over
+pages is not among these operators):
 
     plan = hga_paged_plan(cache.lens, new_tokens, cache.free_pages, cache.free_count,
                           cache.block_table, cache.page_size, n_slots,

@@ -355,12 +355,12 @@ hga_status hga_hostkv_plan_for(const hga_dims *dims, const hga_params *prm,
  * slots, hga_paged_decode attends over the table.  Nothing here reads a length
  * on the host, so a serving step can be captured in a CUDA graph.
  *
- * Limits: page_size a power of two; num_pages * page_size, max_pages *
- * page_size and B * max_pages below 2^31; B and Hq at most 65535; D 64 or 128;
- * for hga_paged_decode also B * Hkv * max_pages * page_size (max_pages * page_size
+ * Limits: B at least 1 (an empty batch is the caller's to skip); page_size a
+ * power of two; num_pages * page_size, max_pages * page_size and B * max_pages
+ * below 2^31; B and Hq at most 65535; D 64 or 128; for hga_paged_decode also B * Hkv * max_pages * page_size (max_pages * page_size
  * at most window + sinks with a window) below 2^36.
- * eps, magnitude and scale are taken in fp32: 0 or a normal number there (about 1.2e-38
- * to 3.4e38; scale times log2 e).
+ * eps, magnitude and scale are taken in fp32: 0 or a normal number there (about
+ * 1.2e-38 to 3.4e38; scale times log2 e).
  * int32 buffers need 4-byte alignment, rows of q, k, v, pages and gradients
  * 16-byte alignment.  Outputs must not overlap inputs except where stated, and
  * calls that share a workspace must not overlap on the GPU. */
@@ -457,7 +457,9 @@ typedef struct hga_qk_io {
 
 /* Per-head RMS norms of queries and keys and the position rotation, in one pass
  * over the projections: y = R_p (x (mean x^2 + eps)^(-1/2) weight), computed in
- * fp32 and rounded once.  dims.B * dims.T tokens (dims.T may be any count).
+ * fp32 and rounded once (a normed row of values above about 1e19, whose squares
+ * pass fp32, comes out as zeros).  dims.B * dims.T tokens, below 2^31 (dims.T may
+ * be any count, 0 included).
  * With rotary_dim == 0 the outputs are what hga_forward takes as raw q, k and v;
  * rotated keys and values go to k_pages and v_pages at slot[t] for
  * hga_paged_decode.  A slot of -1 writes no page row; any other slot outside
