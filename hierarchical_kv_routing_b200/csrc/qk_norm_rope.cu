@@ -112,25 +112,17 @@ template <typename T, int P> struct Raw {
     static constexpr int B = P * (int)sizeof(T) / 4;   // 32-bit words per half: 2 or 4
     uint32_t w[2 * B];
 };
+// (ordinary loads: a read-only one may be moved ahead of the wait for the kernel before)
 template <typename T, int P, bool kInter>
-__device__ __forceinline__ void load_raw(Raw<T, P> &x, const T *row, const Place &p, bool live) {
-    constexpr int B = Raw<T, P>::B;
-#pragma unroll
-    for (int i = 0; i < 2 * B; ++i) x.w[i] = 0u;
-    if (!live) return;
-    if constexpr (B == 4) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + (h ? p.hi : p.lo)));
-            x.w[4 * h] = v.x, x.w[4 * h + 1] = v.y, x.w[4 * h + 2] = v.z, x.w[4 * h + 3] = v.w;
-        }
-    } else if constexpr (kInter) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + p.lo));
+__device__ __forceinline__ void load_raw(Raw<T, P> &x, const T *row, const Place &p) {
+    static_assert(Raw<T, P>::B == 2, "8 bytes a half");
+    if constexpr (kInter) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(row + p.lo);
         x.w[0] = v.x, x.w[1] = v.y, x.w[2] = v.z, x.w[3] = v.w;
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + (h ? p.hi : p.lo)));
+            const uint2 v = *reinterpret_cast<const uint2 *>(row + (h ? p.hi : p.lo));
             x.w[2 * h] = v.x, x.w[2 * h + 1] = v.y;
         }
     }
@@ -242,7 +234,7 @@ __device__ __forceinline__ void trig(const Place &p, const float2 *cs, float (&c
 template <typename T, int P, bool kInter>
 __device__ __forceinline__ void load_weight(Raw<T, P> &x, const void *w, const Place &p) {
     if (w) {
-        load_raw<T, P, kInter>(x, static_cast<const T *>(w), p, true);
+        load_raw<T, P, kInter>(x, static_cast<const T *>(w), p);
         return;
     }
     Pairs<P> y;

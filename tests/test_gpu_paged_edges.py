@@ -200,3 +200,21 @@ def test_an_argument_without_a_truth_value_raises_its_own_error(hga):
     kp, vp, table = pages_for(1, [4], 1, 64, "bf16", 4)
     with pytest.raises(RuntimeError, match="ambiguous"):
         hga.hga_paged_decode(queries(1, 1, 1, 64, "bf16"), kp, vp, table, i32([4]), want_lse=torch.zeros(2))
+
+
+def test_weights_that_the_call_before_writes(hga):
+    """The gradient of a weight as the next call's weight: the call starts while the one
+    before is still running, and reads the weight after it."""
+    g = torch.Generator().manual_seed(3)
+    x, d = (torch.randn(5000, 3, 64, generator=g).cuda() for _ in range(2))
+    w, pos, rope = torch.ones(64, device="cuda"), i32(np.arange(5000)), hga.HGARope()
+    out = torch.empty(5000, 3, 64, device="cuda")
+    for i in range(20):
+        y = x * (i + 1) if i % 2 else x - i
+        torch.cuda.synchronize()
+        _, _, _, dqw, _ = hga.hga_qk_norm_rope_backward(y, y, d, d, pos, rope, q_weight=w, k_weight=w)
+        hga.hga_qk_norm_rope(y, y, None, pos, rope, q_weight=dqw, k_weight=dqw, q_out=out)
+        first = out.clone()
+        torch.cuda.synchronize()
+        hga.hga_qk_norm_rope(y, y, None, pos, rope, q_weight=dqw, k_weight=dqw, q_out=out)
+        assert torch.equal(first, out)
