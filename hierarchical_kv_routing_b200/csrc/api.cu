@@ -390,8 +390,11 @@ hga_status hga_device_status(void *stream, int clear) {
     const unsigned slot = calls.fetch_add(1) % kStatusSlots;
     int first = 0;
     if (e == cudaSuccess) {
-        k_first_error<<<1, 32, 0, st>>>(words, clear, slot);
-        e = cudaGetLastError();
+        cudaLaunchConfig_t cfg = {};             // (its own error, not what an earlier call left)
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(32);
+        cfg.stream = st;
+        e = cudaLaunchKernelEx(&cfg, k_first_error, words, clear, slot);
     }
     if (e == cudaSuccess)
         e = cudaMemcpyFromSymbolAsync(&first, g_status, sizeof(int), slot * sizeof(int),
